@@ -2,7 +2,10 @@
 
 The compute path is the HIP library ``lib/librdfft.so`` (C ABI in
 ``include/rdfft.h``); :mod:`block_circulant_layers_amd.binding` is its thin
-Python binding.  Build with ``python -m block_circulant_layers_amd.build``.
+Python binding.  The operators of a fine-tuning step around the layers are in
+``lib/libfinetune.so`` (C ABI in ``include/finetune.h``) and
+:mod:`block_circulant_layers_amd.finetune`.  Build both with
+``python -m block_circulant_layers_amd.build``.
 """
 
 from .binding import (  # noqa: F401
@@ -31,3 +34,29 @@ from .binding import (  # noqa: F401
     rdfft_unpack,
 )
 from .layer import BlockCirculantFunction, BlockCirculantLinear  # noqa: F401
+from .finetune import (  # noqa: F401
+    IGNORE,
+    FinetuneError,
+    LayerNorm,
+    PolicyLoss,
+    PreferenceLoss,
+    clip_grad_norm,
+    clip_grad_norm_,
+    finetune_lib,
+    finetune_lib_path,
+    grad_norm,
+    layer_norm,
+    layer_norm_bwd,
+    layer_norm_fwd,
+    policy_loss,
+    policy_loss_bwd,
+    policy_loss_fwd,
+    policy_loss_step,
+    preference_loss,
+    preference_loss_bwd,
+    preference_loss_fwd,
+    preference_loss_step,
+    token_logp,
+    token_logprob,
+    token_logprob_bwd,
+)

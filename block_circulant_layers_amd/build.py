@@ -2,9 +2,10 @@
 
     python -m block_circulant_layers_amd.build
 
-Steps: generate csrc/twiddles.inc from float64 math, then one hipcc call for
-librdfft.so and one for libstreamprobe.so (the in-place streaming pass that
-bench.py measures the transforms against).  Packed FP32 instructions are
+Steps: generate csrc/twiddles.inc from float64 math, then one hipcc call each
+for librdfft.so, libfinetune.so (csrc/finetune: the operators of a fine-tuning
+step around the layers) and libstreamprobe.so (the in-place streaming pass
+that bench.py measures the transforms against).  Packed FP32 instructions are
 disabled for all device code.
 
 kernel_resources() reads back, from the built library's own gfx950 code
@@ -24,6 +25,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "librdfft.so")
+# the operators of a fine-tuning step around the layers (include/finetune.h)
+FINETUNE_LIB = os.path.join(LIBDIR, "libfinetune.so")
 # the in-place streaming pass bench.py measures the transforms against
 PROBE_LIB = os.path.join(LIBDIR, "libstreamprobe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -54,6 +57,7 @@ def build(verbose: bool = True) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    build_finetune(verbose)
     tmp = PROBE_LIB + ".tmp"
     cmd = [HIPCC, *HIP_FLAGS, os.path.join(CSRC, "stream_probe.hip"), "-o", tmp]
     if verbose:
@@ -61,6 +65,18 @@ def build(verbose: bool = True) -> str:
     subprocess.run(cmd, check=True)
     os.replace(tmp, PROBE_LIB)
     return LIB
+
+
+def build_finetune(verbose: bool = True) -> str:
+    os.makedirs(LIBDIR, exist_ok=True)
+    tmp = FINETUNE_LIB + ".tmp"
+    cmd = [HIPCC, *HIP_FLAGS, "-I", os.path.join(ROOT, "include"),
+           os.path.join(CSRC, "finetune", "finetune_lib.hip"), "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, FINETUNE_LIB)
+    return FINETUNE_LIB
 
 
 def kernel_resources(lib: str = LIB) -> dict:

@@ -1,0 +1,424 @@
+// finetune_lib.hip -- C ABI of libfinetune.so: argument checks, kernel selection, launches.
+#include <hip/hip_runtime.h>
+
+#include "finetune.h"
+#include "grad_clip.hpp"
+#include "layer_norm.hpp"
+#include "logit_loss.hpp"
+#include "validate.hpp"
+
+namespace finetune {
+namespace {
+
+int launch_status() { return hipGetLastError() == hipSuccess ? RDFFT_OK : RDFFT_ERR_LAUNCH; }
+
+template <class F>
+int by_dtype(int64_t dtype, F f) {
+  switch (dtype) {
+    case RDFFT_F32: return f(F32{});
+    case RDFFT_BF16: return f(Bf16{});
+    default: return f(F16{});
+  }
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t kMaxGrid = 1 << 20;
+unsigned grid_of(int64_t n) { return static_cast<unsigned>(n < kMaxGrid ? n : kMaxGrid); }
+
+// ---- layer normalisation --------------------------------------------------
+
+struct DwSplit {
+  int64_t parts, per;
+};
+DwSplit dw_split(int64_t rows, int64_t d) {
+  const int64_t cols = ceil_div(d, kNormThreads);
+  int64_t parts = std::min<int64_t>(std::max<int64_t>(1024 / cols, 1), ceil_div(rows, 16));
+  if (parts < 1) parts = 1;
+  const int64_t per = std::max<int64_t>(ceil_div(rows, parts), 1);
+  return {std::max<int64_t>(ceil_div(rows, per), 1), per};
+}
+
+// ---- logits ---------------------------------------------------------------
+
+template <class Io>
+Rows<Io> rows_of(const finetune_logits* in) {
+  return {static_cast<typename Io::T*>(const_cast<void*>(in->data)), in->seq_stride, in->pos_stride};
+}
+template <class Io>
+Rows<Io> rows_of(const finetune_dlogits* out) {
+  return {static_cast<typename Io::T*>(out->data), out->seq_stride, out->pos_stride};
+}
+
+int launch_logprob(const finetune_logits* in, float* logp, float* lse, hipStream_t s) {
+  const int64_t rows = logit_rows(in);
+  if (rows == 0) return RDFFT_OK;
+  return by_dtype(in->dtype, [&](auto io) {
+    using Io = decltype(io);
+    hipLaunchKernelGGL((token_logprob_kernel<Io>), dim3(grid_of(rows)), dim3(kLogitThreads), 0, s, rows_of<Io>(in),
+                       in->labels, logp, lse, rows, in->positions, static_cast<int>(in->vocab));
+    return launch_status();
+  });
+}
+
+int launch_grad(const finetune_logits* in, const float* lse, const RowScale& scale, const finetune_dlogits* out,
+                hipStream_t s) {
+  const int64_t rows = logit_rows(in);
+  if (rows == 0) return RDFFT_OK;
+  return by_dtype(in->dtype, [&](auto io) {
+    using Io = decltype(io);
+    hipLaunchKernelGGL((logits_grad_kernel<Io>), dim3(grid_of(rows)), dim3(kLogitThreads), 0, s, rows_of<Io>(in),
+                       in->labels, lse, scale, rows_of<Io>(out), rows, in->positions, static_cast<int>(in->vocab));
+    return launch_status();
+  });
+}
+
+int64_t logits_workspace(const finetune_logits* in) { return (in->seqs * 4 + 15) / 16 * 16; }  // counts
+
+int launch_preference(const finetune_logits* in, const float* ref, const finetune_preference* how, float* loss,
+                      float* logratio, float* logp, float* lse, float* slope, hipStream_t s) {
+  const int st = launch_logprob(in, logp, lse, s);
+  if (st != RDFFT_OK || in->seqs == 0) return st;
+  const Preference p{static_cast<int>(how->kind), how->average != 0, how->beta, how->smoothing};
+  const int64_t pairs = in->seqs / 2;
+  hipLaunchKernelGGL((preference_kernel), dim3(grid_of(pairs)), dim3(kLogitThreads), 0, s, in->labels, logp, ref, p,
+                     loss, logratio, slope, pairs, in->positions);
+  return launch_status();
+}
+
+int launch_policy(const finetune_logits* in, const float* old, const float* ref, const float* adv,
+                  const finetune_policy* how, float* stats, float* logp, float* lse, float* slope, void* ws,
+                  hipStream_t s) {
+  int st = launch_logprob(in, logp, lse, s);
+  if (st != RDFFT_OK) return st;
+  auto* counts = static_cast<int*>(ws);
+  if (in->seqs > 0) {
+    hipLaunchKernelGGL((count_kernel), dim3(grid_of(in->seqs)), dim3(kLogitThreads), 0, s, in->labels, counts,
+                       in->seqs, in->positions);
+    st = launch_status();
+    if (st != RDFFT_OK) return st;
+  }
+  const Policy p{static_cast<int>(how->reduction), how->advantage_per_token != 0, how->clip_low, how->clip_high,
+                 how->kl_coef};
+  hipLaunchKernelGGL((policy_kernel), dim3(1), dim3(kLogitThreads), 0, s, in->labels, logp, old, ref, adv, counts, p,
+                     stats, slope, in->seqs, in->positions);
+  return launch_status();
+}
+
+// ---- gradient tensors -----------------------------------------------------
+
+int64_t clip_chunks(const finetune_tensor* t, int64_t n) {
+  int64_t c = 0;
+  for (int64_t i = 0; i < n; ++i) c += ceil_div(t[i].count, kClipChunk);
+  return c;
+}
+
+// f(table, first chunk of the launch, chunks) for tables of up to kClipTensors tensors
+template <class F>
+int for_tables(const finetune_tensor* t, int64_t n, F f) {
+  ClipTable table;
+  table.n = 0;
+  table.first[0] = 0;
+  int64_t base = 0;
+  auto flush = [&]() {
+    if (table.n == 0) return static_cast<int>(RDFFT_OK);
+    const int chunks = table.first[table.n];
+    const int st = f(table, base, chunks);
+    base += chunks;
+    table.n = 0;
+    return st;
+  };
+  for (int64_t i = 0; i < n; ++i) {
+    int64_t left = t[i].count;
+    const int64_t e = dtype_bytes(static_cast<int>(t[i].dtype));
+    const char* g = static_cast<const char*>(t[i].grad);
+    char* o = static_cast<char*>(t[i].out);
+    while (left > 0) {
+      // chunk numbers of a launch stay below 2^24
+      const int64_t take = std::min<int64_t>(left, int64_t(kClipChunk) << 20);
+      const int k = table.n++;
+      table.in[k] = g;
+      table.out[k] = o;
+      table.count[k] = take;
+      table.dtype[k] = static_cast<int8_t>(t[i].dtype);
+      table.first[k + 1] = table.first[k] + static_cast<int>(ceil_div(take, kClipChunk));
+      left -= take;
+      g += take * e;
+      if (o) o += take * e;
+      if (table.n == kClipTensors || table.first[table.n] >= (1 << 23)) {
+        const int st = flush();
+        if (st != RDFFT_OK) return st;
+      }
+    }
+  }
+  return flush();
+}
+
+int64_t clip_workspace(const finetune_tensor* t, int64_t n) { return 16 + (clip_chunks(t, n) * 8 + 15) / 16 * 16; }
+
+int launch_norm(const finetune_tensor* t, int64_t n, double max_norm, double eps, float* norm, void* ws,
+                bool with_factor, hipStream_t s) {
+  auto* partial = reinterpret_cast<double*>(static_cast<char*>(ws) + 16);
+  int st = for_tables(t, n, [&](const ClipTable& table, int64_t base, int chunks) {
+    hipLaunchKernelGGL((grad_square_kernel), dim3(static_cast<unsigned>(chunks)), dim3(kClipThreads), 0, s, table,
+                       partial + base);
+    return launch_status();
+  });
+  if (st != RDFFT_OK) return st;
+  hipLaunchKernelGGL((grad_norm_kernel), dim3(1), dim3(kClipThreads), 0, s, partial, clip_chunks(t, n), max_norm, eps,
+                     norm, with_factor ? static_cast<float*>(ws) : nullptr);
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace finetune
+
+using namespace finetune;
+
+extern "C" {
+
+int finetune_abi_version(void) { return FINETUNE_ABI_VERSION; }
+
+const char* finetune_status_string(int status) {
+  switch (status) {
+    case RDFFT_OK: return "ok";
+    case RDFFT_ERR_NULL: return "null pointer";
+    case RDFFT_ERR_SIZE: return "a count or parameter outside its range, or a workspace too small";
+    case RDFFT_ERR_SHAPE: return "strides or counts that do not go together";
+    case RDFFT_ERR_DTYPE: return "unsupported dtype";
+    case RDFFT_ERR_ALIGN: return "a pointer without its element's alignment";
+    case RDFFT_ERR_ALIAS: return "output buffer overlaps another buffer";
+    case RDFFT_ERR_LAUNCH: return "kernel launch failed";
+    default: return "unknown status";
+  }
+}
+
+int layer_norm_fwd(const void* x, const float* weight, const float* bias, void* y, float* mean, float* rstd,
+                   int64_t rows, int64_t d, int64_t x_stride, int64_t y_stride, double eps, int dtype, void* stream) {
+  const int st = check_norm_fwd(x, weight, bias, y, mean, rstd, rows, d, x_stride, y_stride, eps, dtype);
+  if (st != RDFFT_OK || rows == 0) return st;
+  return by_dtype(dtype, [&](auto io) {
+    using Io = decltype(io);
+    using T = typename Io::T;
+    hipLaunchKernelGGL((layer_norm_fwd_kernel<Io>), dim3(grid_of(rows)), dim3(kNormThreads), 0,
+                       static_cast<hipStream_t>(stream), static_cast<const T*>(x), weight, bias, static_cast<T*>(y),
+                       mean, rstd, rows, static_cast<int>(d), x_stride, y_stride, static_cast<float>(eps));
+    return launch_status();
+  });
+}
+
+int layer_norm_bwd_workspace(int64_t rows, int64_t d, int64_t* bytes) {
+  if (bytes == nullptr) return RDFFT_ERR_NULL;
+  const int st = check_norm_dims(rows, d);
+  if (st == RDFFT_OK) *bytes = rows == 0 ? 0 : (dw_split(rows, d).parts * 2 * d * 4 + 15) / 16 * 16;
+  return st;
+}
+
+int layer_norm_bwd(const void* x, const float* weight, const float* mean, const float* rstd, const void* dy, void* dx,
+                   float* dweight, float* dbias, void* ws, int64_t ws_bytes, int64_t rows, int64_t d,
+                   int64_t x_stride, int64_t dy_stride, int64_t dx_stride, int dtype, void* stream) {
+  int64_t need = 0;
+  int st = layer_norm_bwd_workspace(rows, d, &need);
+  if (st == RDFFT_OK || !valid_dtype(dtype))
+    st = check_norm_bwd(x, weight, mean, rstd, dy, dx, dweight, dbias, ws, ws_bytes, need, rows, d, x_stride,
+                        dy_stride, dx_stride, dtype);
+  if (st != RDFFT_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int n = static_cast<int>(d);
+  auto* part = static_cast<float*>(ws);
+  const DwSplit split = dw_split(rows, d);
+  // the sums over rows first: dx may replace the dy they read
+  if (dweight || dbias) {
+    if (rows > 0) {
+      st = by_dtype(dtype, [&](auto io) {
+        using Io = decltype(io);
+        using T = typename Io::T;
+        hipLaunchKernelGGL((layer_norm_dw_kernel<Io>),
+                           dim3(static_cast<unsigned>(ceil_div(d, kNormThreads)), static_cast<unsigned>(split.parts)),
+                           dim3(kNormThreads), 0, s, static_cast<const T*>(x), mean, rstd,
+                           static_cast<const T*>(dy), part, rows, n, x_stride, dy_stride, split.per);
+        return launch_status();
+      });
+      if (st != RDFFT_OK) return st;
+    }
+    hipLaunchKernelGGL((layer_norm_dw_sum_kernel), dim3(static_cast<unsigned>(ceil_div(d, kNormThreads))),
+                       dim3(kNormThreads), 0, s, part, dweight, dbias, n,
+                       rows > 0 ? static_cast<int>(split.parts) : 0);
+    st = launch_status();
+  }
+  if (st != RDFFT_OK || !dx || rows == 0) return st;
+  return by_dtype(dtype, [&](auto io) {
+    using Io = decltype(io);
+    using T = typename Io::T;
+    hipLaunchKernelGGL((layer_norm_dx_kernel<Io>), dim3(grid_of(rows)), dim3(kNormThreads), 0, s,
+                       static_cast<const T*>(x), weight, mean, rstd, static_cast<const T*>(dy), static_cast<T*>(dx),
+                       rows, n, x_stride, dy_stride, dx_stride);
+    return launch_status();
+  });
+}
+
+int finetune_logits_workspace(const finetune_logits* in, int64_t* bytes) {
+  if (bytes == nullptr) return RDFFT_ERR_NULL;
+  const int st = check_logits_dims(in);
+  if (st == RDFFT_OK) *bytes = logits_workspace(in);
+  return st;
+}
+
+int token_logprob(const finetune_logits* in, float* logp, float* lse, void* ws, int64_t ws_bytes, void* stream) {
+  int st = check_logits(in);
+  if (st != RDFFT_OK) return st;
+  const int64_t rows = logit_rows(in), need = logits_workspace(in);
+  st = check_workspace(ws, ws_bytes, need);
+  const Array none[] = {{nullptr, 0}}, outs[] = {{logp, rows}, {lse, rows}};
+  if (st == RDFFT_OK) st = check_arrays(in, nullptr, none, outs, ws, need);
+  if (st != RDFFT_OK) return st;
+  return launch_logprob(in, logp, lse, static_cast<hipStream_t>(stream));
+}
+
+int token_logprob_bwd(const finetune_logits* in, const float* lse, const float* dlogp, const finetune_dlogits* out,
+                      void* stream) {
+  int st = check_logits(in);
+  if (st == RDFFT_OK) st = check_dlogits(in, out);
+  if (st != RDFFT_OK) return st;
+  const int64_t rows = logit_rows(in);
+  const Array ins[] = {{lse, rows}, {dlogp, rows}}, none[] = {{nullptr, 0}};
+  st = check_arrays(in, out, ins, none, nullptr, 0);
+  if (st != RDFFT_OK) return st;
+  return launch_grad(in, lse, RowScale{nullptr, dlogp, 1.0f, 1, true}, out, static_cast<hipStream_t>(stream));
+}
+
+int preference_loss_fwd(const finetune_logits* in, const float* ref_logp, const finetune_preference* how, float* loss,
+                        float* logratio, float* logp, float* lse, float* slope, void* ws, int64_t ws_bytes,
+                        void* stream) {
+  int st = check_logits(in);
+  if (st == RDFFT_OK) st = check_preference(in, how);
+  if (st != RDFFT_OK) return st;
+  const int64_t rows = logit_rows(in), need = logits_workspace(in);
+  st = check_workspace(ws, ws_bytes, need);
+  const Array ins[] = {{ref_logp, rows}};
+  const Array outs[] = {{loss, in->seqs / 2}, {logratio, in->seqs}, {logp, rows}, {lse, rows}, {slope, in->seqs}};
+  if (st == RDFFT_OK) st = check_arrays(in, nullptr, ins, outs, ws, need);
+  if (st != RDFFT_OK) return st;
+  return launch_preference(in, ref_logp, how, loss, logratio, logp, lse, slope, static_cast<hipStream_t>(stream));
+}
+
+int preference_loss_bwd(const finetune_logits* in, const float* lse, const float* slope, const float* dloss,
+                        const finetune_dlogits* out, void* stream) {
+  int st = check_logits(in);
+  if (st == RDFFT_OK && in->seqs % 2 != 0) st = RDFFT_ERR_SHAPE;
+  if (st == RDFFT_OK) st = check_dlogits(in, out);
+  if (st != RDFFT_OK) return st;
+  const Array ins[] = {{lse, logit_rows(in)}, {slope, in->seqs}, {dloss, in->seqs / 2}}, none[] = {{nullptr, 0}};
+  st = check_arrays(in, out, ins, none, nullptr, 0);
+  if (st != RDFFT_OK) return st;
+  return launch_grad(in, lse, RowScale{dloss, slope, 1.0f, in->seqs / 2, false}, out,
+                     static_cast<hipStream_t>(stream));
+}
+
+int preference_loss_step(const finetune_logits* in, const float* ref_logp, const finetune_preference* how,
+                         double scale, float* loss, float* logratio, float* logp, float* lse, float* slope,
+                         const finetune_dlogits* out, void* ws, int64_t ws_bytes, void* stream) {
+  int st = check_logits(in);
+  if (st == RDFFT_OK) st = check_preference(in, how);
+  if (st == RDFFT_OK) st = check_dlogits(in, out);
+  if (st != RDFFT_OK) return st;
+  const int64_t rows = logit_rows(in), need = logits_workspace(in);
+  st = check_workspace(ws, ws_bytes, need);
+  const Array ins[] = {{ref_logp, rows}};
+  const Array outs[] = {{loss, in->seqs / 2}, {logratio, in->seqs}, {logp, rows}, {lse, rows}, {slope, in->seqs}};
+  if (st == RDFFT_OK) st = check_arrays(in, out, ins, outs, ws, need);
+  if (st != RDFFT_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  st = launch_preference(in, ref_logp, how, loss, logratio, logp, lse, slope, s);
+  if (st != RDFFT_OK) return st;
+  return launch_grad(in, lse, RowScale{nullptr, slope, static_cast<float>(scale), 1, false}, out, s);
+}
+
+int policy_loss_fwd(const finetune_logits* in, const float* old_logp, const float* ref_logp, const float* advantages,
+                    const finetune_policy* how, float* stats, float* logp, float* lse, float* slope, void* ws,
+                    int64_t ws_bytes, void* stream) {
+  int st = check_logits(in);
+  if (st == RDFFT_OK) st = check_policy(how);
+  if (st != RDFFT_OK) return st;
+  const int64_t rows = logit_rows(in), need = logits_workspace(in);
+  st = check_workspace(ws, ws_bytes, need);
+  const Array ins[] = {{old_logp, rows}, {ref_logp, rows, true}, {advantages, how->advantage_per_token ? rows : in->seqs}};
+  const Array outs[] = {{stats, 2}, {logp, rows}, {lse, rows}, {slope, rows}};
+  if (st == RDFFT_OK) st = check_arrays(in, nullptr, ins, outs, ws, need);
+  if (st != RDFFT_OK) return st;
+  return launch_policy(in, old_logp, ref_logp, advantages, how, stats, logp, lse, slope, ws,
+                       static_cast<hipStream_t>(stream));
+}
+
+int policy_loss_bwd(const finetune_logits* in, const float* lse, const float* slope, const float* dloss,
+                    const finetune_dlogits* out, void* stream) {
+  int st = check_logits(in);
+  if (st == RDFFT_OK) st = check_dlogits(in, out);
+  if (st != RDFFT_OK) return st;
+  const int64_t rows = logit_rows(in);
+  const Array ins[] = {{lse, rows}, {slope, rows}, {dloss, 1}}, none[] = {{nullptr, 0}};
+  st = check_arrays(in, out, ins, none, nullptr, 0);
+  if (st != RDFFT_OK) return st;
+  return launch_grad(in, lse, RowScale{dloss, slope, 1.0f, 1, true}, out, static_cast<hipStream_t>(stream));
+}
+
+int policy_loss_step(const finetune_logits* in, const float* old_logp, const float* ref_logp, const float* advantages,
+                     const finetune_policy* how, double scale, float* stats, float* logp, float* lse, float* slope,
+                     const finetune_dlogits* out, void* ws, int64_t ws_bytes, void* stream) {
+  int st = check_logits(in);
+  if (st == RDFFT_OK) st = check_policy(how);
+  if (st == RDFFT_OK) st = check_dlogits(in, out);
+  if (st != RDFFT_OK) return st;
+  const int64_t rows = logit_rows(in), need = logits_workspace(in);
+  st = check_workspace(ws, ws_bytes, need);
+  const Array ins[] = {{old_logp, rows}, {ref_logp, rows, true}, {advantages, how->advantage_per_token ? rows : in->seqs}};
+  const Array outs[] = {{stats, 2}, {logp, rows}, {lse, rows}, {slope, rows}};
+  if (st == RDFFT_OK) st = check_arrays(in, out, ins, outs, ws, need);
+  if (st != RDFFT_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  st = launch_policy(in, old_logp, ref_logp, advantages, how, stats, logp, lse, slope, ws, s);
+  if (st != RDFFT_OK) return st;
+  return launch_grad(in, lse, RowScale{nullptr, slope, static_cast<float>(scale), 1, true}, out, s);
+}
+
+int grad_norm_workspace(const finetune_tensor* tensors, int64_t n, int64_t* bytes) {
+  if (bytes == nullptr) return RDFFT_ERR_NULL;
+  if (n < 0 || n > kMaxTensors) return RDFFT_ERR_SIZE;
+  if (n > 0 && tensors == nullptr) return RDFFT_ERR_NULL;
+  int64_t total = 0;
+  for (int64_t i = 0; i < n; ++i)
+    if (tensors[i].count < 0 || tensors[i].count > kMaxElems || (total += tensors[i].count) > kMaxElems)
+      return RDFFT_ERR_SIZE;
+  *bytes = clip_workspace(tensors, n);
+  return RDFFT_OK;
+}
+
+int grad_norm(const finetune_tensor* tensors, int64_t n, float* norm, void* ws, int64_t ws_bytes, void* stream) {
+  int st = check_tensors(tensors, n, false);
+  if (st == RDFFT_OK && norm == nullptr) st = RDFFT_ERR_NULL;
+  if (st == RDFFT_OK && !aligned_to(norm, 4)) st = RDFFT_ERR_ALIGN;
+  if (st == RDFFT_OK) st = check_workspace(ws, ws_bytes, clip_workspace(tensors, n));
+  if (st != RDFFT_OK) return st;
+  return launch_norm(tensors, n, 0.0, 0.0, norm, ws, false, static_cast<hipStream_t>(stream));
+}
+
+int clip_grad_norm(const finetune_tensor* tensors, int64_t n, double max_norm, double eps, float* norm, void* ws,
+                   int64_t ws_bytes, void* stream) {
+  int st = check_tensors(tensors, n, true);
+  if (st == RDFFT_OK && (!(max_norm >= 0.0) || !(eps >= 0.0))) st = RDFFT_ERR_SIZE;
+  if (st == RDFFT_OK && norm == nullptr) st = RDFFT_ERR_NULL;
+  if (st == RDFFT_OK && !aligned_to(norm, 4)) st = RDFFT_ERR_ALIGN;
+  if (st == RDFFT_OK) st = check_workspace(ws, ws_bytes, clip_workspace(tensors, n));
+  if (st == RDFFT_OK) st = check_tensor_aliases(tensors, n);
+  if (st != RDFFT_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  st = launch_norm(tensors, n, max_norm, eps, norm, ws, true, s);
+  if (st != RDFFT_OK) return st;
+  return for_tables(tensors, n, [&](const ClipTable& table, int64_t, int chunks) {
+    hipLaunchKernelGGL((grad_scale_kernel), dim3(static_cast<unsigned>(chunks)), dim3(kClipThreads), 0, s, table,
+                       static_cast<const float*>(ws));
+    return launch_status();
+  });
+}
+
+}  // extern "C"
