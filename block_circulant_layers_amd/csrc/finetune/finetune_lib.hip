@@ -1,6 +1,8 @@
 // finetune_lib.hip -- C ABI of libfinetune.so: argument checks, kernel selection, launches.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "finetune.h"
 #include "grad_clip.hpp"
 #include "layer_norm.hpp"
@@ -28,15 +30,99 @@ unsigned grid_of(int64_t n) { return static_cast<unsigned>(n < kMaxGrid ? n : kM
 
 // ---- layer normalisation --------------------------------------------------
 
+// threads that hold a row of d elements, 0 for the kernels of any length
+int norm_threads(int64_t d) {
+  for (int t : {8, 64, 256, 1024})
+    if (d <= t * kNormElems) return t;
+  return 0;
+}
+
+// f(std::integral_constant<int, T>, std::bool_constant<RAGGED>) for a row of d elements of Io
+template <class Io, class F>
+void by_norm_row(int64_t d, F f) {
+  auto ragged = [&](auto t) {
+    if (d % Io::kVec)
+      f(t, std::true_type{});
+    else
+      f(t, std::false_type{});
+  };
+  switch (norm_threads(d)) {
+    case 8: ragged(std::integral_constant<int, 8>{}); break;
+    case 64: ragged(std::integral_constant<int, 64>{}); break;
+    case 256: ragged(std::integral_constant<int, 256>{}); break;
+    default: ragged(std::integral_constant<int, 1024>{}); break;
+  }
+}
+
+// Workgroups of the backward, each with one slice of the sums over rows (the
+// kernels of any length: row ranges of the column kernel).  512 workgroups of
+// 256 threads keep enough loads in flight to fill the memory system; more
+// would only make more slices to sum.
 struct DwSplit {
   int64_t parts, per;
 };
 DwSplit dw_split(int64_t rows, int64_t d) {
+  const int t = norm_threads(d);
+  if (t) {
+    const int64_t groups = ceil_div(std::max<int64_t>(rows, 1), norm_wg(t) / t);
+    return {std::min<int64_t>(groups, t == 1024 ? 256 : 512), 0};
+  }
   const int64_t cols = ceil_div(d, kNormThreads);
-  int64_t parts = std::min<int64_t>(std::max<int64_t>(1024 / cols, 1), ceil_div(rows, 16));
-  if (parts < 1) parts = 1;
+  const int64_t parts = std::max<int64_t>(std::min<int64_t>(1024 / cols, ceil_div(rows, 16)), 1);
   const int64_t per = std::max<int64_t>(ceil_div(rows, parts), 1);
   return {std::max<int64_t>(ceil_div(rows, per), 1), per};
+}
+
+template <class Io>
+int launch_norm_fwd(const void* x, const float* w, const float* b, void* y, float* mean, float* rstd, int64_t rows,
+                    int64_t d, int64_t xs, int64_t ys, double eps, hipStream_t s) {
+  using T = typename Io::T;
+  const auto* px = static_cast<const T*>(x);
+  auto* py = static_cast<T*>(y);
+  const int n = static_cast<int>(d);
+  if (norm_threads(d) == 0) {
+    hipLaunchKernelGGL((layer_norm_wide_fwd_kernel<Io>), dim3(grid_of(rows)), dim3(kNormThreads), 0, s, px, w, b, py,
+                       mean, rstd, rows, n, xs, ys, static_cast<float>(eps));
+    return launch_status();
+  }
+  by_norm_row<Io>(d, [&](auto t, auto ragged) {
+    constexpr int TT = decltype(t)::value, WG = norm_wg(TT);
+    const int64_t groups = ceil_div(rows, WG / TT);
+    const int64_t grid = std::min<int64_t>(groups, TT == 1024 ? 512 : 2048);
+    hipLaunchKernelGGL((layer_norm_fwd_kernel<Io, TT, decltype(ragged)::value>), dim3(static_cast<unsigned>(grid)),
+                       dim3(WG), 0, s, px, w, b, py, mean, rstd, rows, n, xs, ys, static_cast<float>(eps));
+  });
+  return launch_status();
+}
+
+template <class Io>
+int launch_norm_bwd(const void* x, const float* w, const float* mean, const float* rstd, const void* dy, void* dx,
+                    float* ws, const DwSplit& split, int64_t rows, int64_t d, int64_t xs, int64_t dys, int64_t dxs,
+                    hipStream_t s) {
+  using T = typename Io::T;
+  const auto *px = static_cast<const T*>(x), *pg = static_cast<const T*>(dy);
+  auto* po = static_cast<T*>(dx);
+  const int n = static_cast<int>(d);
+  if (norm_threads(d)) {
+    by_norm_row<Io>(d, [&](auto t, auto ragged) {
+      constexpr int TT = decltype(t)::value;
+      hipLaunchKernelGGL((layer_norm_bwd_kernel<Io, TT, decltype(ragged)::value>),
+                         dim3(static_cast<unsigned>(split.parts)), dim3(norm_wg(TT)), norm_bwd_lds(TT), s, px, w, mean, rstd, pg, po,
+                         ws, rows, n, xs, dys, dxs);
+    });
+    return launch_status();
+  }
+  if (ws) {  // the sums first: dx may replace the dy they read
+    hipLaunchKernelGGL((layer_norm_wide_dw_kernel<Io>),
+                       dim3(static_cast<unsigned>(ceil_div(d, kNormThreads)), static_cast<unsigned>(split.parts)),
+                       dim3(kNormThreads), 0, s, px, mean, rstd, pg, ws, rows, n, xs, dys, split.per);
+    const int st = launch_status();
+    if (st != RDFFT_OK) return st;
+  }
+  if (po)
+    hipLaunchKernelGGL((layer_norm_wide_dx_kernel<Io>), dim3(grid_of(rows)), dim3(kNormThreads), 0, s, px, w, mean,
+                       rstd, pg, po, rows, n, xs, dys, dxs);
+  return launch_status();
 }
 
 // ---- logits ---------------------------------------------------------------
@@ -198,12 +284,8 @@ int layer_norm_fwd(const void* x, const float* weight, const float* bias, void* 
   const int st = check_norm_fwd(x, weight, bias, y, mean, rstd, rows, d, x_stride, y_stride, eps, dtype);
   if (st != RDFFT_OK || rows == 0) return st;
   return by_dtype(dtype, [&](auto io) {
-    using Io = decltype(io);
-    using T = typename Io::T;
-    hipLaunchKernelGGL((layer_norm_fwd_kernel<Io>), dim3(grid_of(rows)), dim3(kNormThreads), 0,
-                       static_cast<hipStream_t>(stream), static_cast<const T*>(x), weight, bias, static_cast<T*>(y),
-                       mean, rstd, rows, static_cast<int>(d), x_stride, y_stride, static_cast<float>(eps));
-    return launch_status();
+    return launch_norm_fwd<decltype(io)>(x, weight, bias, y, mean, rstd, rows, d, x_stride, y_stride, eps,
+                                         static_cast<hipStream_t>(stream));
   });
 }
 
@@ -224,37 +306,20 @@ int layer_norm_bwd(const void* x, const float* weight, const float* mean, const 
                         dy_stride, dx_stride, dtype);
   if (st != RDFFT_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int n = static_cast<int>(d);
-  auto* part = static_cast<float*>(ws);
   const DwSplit split = dw_split(rows, d);
-  // the sums over rows first: dx may replace the dy they read
-  if (dweight || dbias) {
-    if (rows > 0) {
-      st = by_dtype(dtype, [&](auto io) {
-        using Io = decltype(io);
-        using T = typename Io::T;
-        hipLaunchKernelGGL((layer_norm_dw_kernel<Io>),
-                           dim3(static_cast<unsigned>(ceil_div(d, kNormThreads)), static_cast<unsigned>(split.parts)),
-                           dim3(kNormThreads), 0, s, static_cast<const T*>(x), mean, rstd,
-                           static_cast<const T*>(dy), part, rows, n, x_stride, dy_stride, split.per);
-        return launch_status();
-      });
-      if (st != RDFFT_OK) return st;
-    }
-    hipLaunchKernelGGL((layer_norm_dw_sum_kernel), dim3(static_cast<unsigned>(ceil_div(d, kNormThreads))),
-                       dim3(kNormThreads), 0, s, part, dweight, dbias, n,
-                       rows > 0 ? static_cast<int>(split.parts) : 0);
-    st = launch_status();
+  const bool sums = dweight || dbias;
+  if (rows > 0) {
+    st = by_dtype(dtype, [&](auto io) {
+      return launch_norm_bwd<decltype(io)>(x, weight, mean, rstd, dy, dx, sums ? static_cast<float*>(ws) : nullptr,
+                                           split, rows, d, x_stride, dy_stride, dx_stride, s);
+    });
+    if (st != RDFFT_OK) return st;
   }
-  if (st != RDFFT_OK || !dx || rows == 0) return st;
-  return by_dtype(dtype, [&](auto io) {
-    using Io = decltype(io);
-    using T = typename Io::T;
-    hipLaunchKernelGGL((layer_norm_dx_kernel<Io>), dim3(grid_of(rows)), dim3(kNormThreads), 0, s,
-                       static_cast<const T*>(x), weight, mean, rstd, static_cast<const T*>(dy), static_cast<T*>(dx),
-                       rows, n, x_stride, dy_stride, dx_stride);
-    return launch_status();
-  });
+  if (!sums) return RDFFT_OK;
+  hipLaunchKernelGGL((layer_norm_dw_sum_kernel), dim3(static_cast<unsigned>(ceil_div(2 * d, kSumCols))),
+                     dim3(kSumCols * kSumGroups), 0, s, static_cast<const float*>(ws), dweight, dbias,
+                     static_cast<int>(d), rows > 0 ? static_cast<int>(split.parts) : 0);
+  return launch_status();
 }
 
 int finetune_logits_workspace(const finetune_logits* in, int64_t* bytes) {

@@ -12,12 +12,236 @@ namespace finetune {
 
 constexpr int kNormThreads = 256;
 
-// One workgroup per row.  The variance is the mean square of x - mean (a
+// A row is held by T threads, E elements each, in 16-byte pieces: piece i of
+// thread t holds columns (i T + t) V .. + V.  T = 8, 64, 256 and 1024 with 16
+// elements a thread cover rows of up to 128, 1024, 4096 and 16384 elements; a
+// workgroup of 256 (1024) threads holds 256 / T rows at once and walks over the
+// rows, so that weight, bias and the sums over rows stay on the chip.
+constexpr int kNormElems = 16;
+constexpr int norm_wg(int t) { return t > kNormThreads ? t : kNormThreads; }
+
+// RAGGED: the row's length is no multiple of a piece, so a piece may be cut.
+template <class Io, int T, bool RAGGED>
+struct NormRow {
+  static constexpr int V = Io::kVec;
+  static constexpr int E = kNormElems;
+  static constexpr int N = E / V;  // pieces a thread
+  typename Io::Vec raw[N];
+
+  static __device__ __forceinline__ int col(int i) { return (i * T + static_cast<int>(threadIdx.x) % T) * V; }
+  // whether element e of piece i lies in the row
+  static __device__ __forceinline__ bool has(int i, int e, int d) {
+    return RAGGED ? col(i) + e < d : col(i) < d;
+  }
+  __device__ __forceinline__ void load(const typename Io::T* p, int d) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = col(i);
+      raw[i] = {};
+      if (c + V <= d) {
+        raw[i] = *reinterpret_cast<const typename Io::Vec*>(p + c);
+      } else if (RAGGED && c < d) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (c + e < d) raw[i][e] = p[c + e];
+      }
+    }
+  }
+  __device__ __forceinline__ float at(int k) const { return Io::widen(raw[k / V][k % V]); }
+  static __device__ __forceinline__ void store(typename Io::T* p, int d, const float* v) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = col(i);
+      typename Io::Vec o;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = Io::narrow(v[i * V + e]);
+      if (c + V <= d) {
+        *reinterpret_cast<typename Io::Vec*>(p + c) = o;
+      } else if (RAGGED && c < d) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (c + e < d) p[c + e] = o[e];
+      }
+    }
+  }
+  // fp32 parameters of the thread's columns, `fill` where there are none
+  static __device__ __forceinline__ void params(const float* p, int d, float fill, float* v) {
+    typedef float Vec __attribute__((ext_vector_type(V), aligned(4)));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = col(i);
+      Vec q = fill;
+      if (p && c + V <= d) {
+        q = *reinterpret_cast<const Vec*>(p + c);
+      } else if (RAGGED && p) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (c + e < d) q[e] = p[c + e];
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[i * V + e] = q[e];
+    }
+  }
+};
+
+// y, mean and rstd.  The variance is the mean square of x - mean, taken from
+// the registers, not E x^2 - mean^2, which cancels for rows whose mean is
+// large against their spread.  The next row's loads are in flight while a row
+// is summed.
+template <class Io, int T, bool RAGGED>
+__global__ void __launch_bounds__(norm_wg(T))
+    layer_norm_fwd_kernel(const typename Io::T* x, const float* w, const float* b, typename Io::T* y, float* mean,
+                          float* rstd, int64_t rows, int d, int64_t xs, int64_t ys, float eps) {
+  using Row = NormRow<Io, T, RAGGED>;
+  constexpr int WG = norm_wg(T), G = WG / T, E = Row::E;
+  __shared__ float s[2][WG / kWave];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  float wr[E], br[E];
+  Row::params(w, d, 1.0f, wr);
+  Row::params(b, d, 0.0f, br);
+  const float n = static_cast<float>(d);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * G;
+  Row next;
+  int64_t r = first + threadIdx.x / T;
+  if (r < rows) next.load(x + r * xs, d);
+  // every thread of the workgroup makes the same number of rounds (barriers inside)
+  for (int64_t r0 = first; r0 < rows; r0 += step, r += step) {
+    const Row cur = next;
+    if (r + step < rows) next.load(x + (r + step) * xs, d);
+    float v[E], a = 0.0f;
+#pragma unroll
+    for (int k = 0; k < E; ++k) a += v[k] = cur.at(k);
+    const float mu = group_sum<T>(a, s[0]) / n;
+    a = 0.0f;
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      v[k] = Row::has(k / Row::V, k % Row::V, d) ? v[k] - mu : 0.0f;
+      a += v[k] * v[k];
+    }
+    const float rs = 1.0f / sqrtf(group_sum<T>(a, s[1]) / n + eps);
+    if (r < rows) {
+      if (threadIdx.x % T == 0) {
+        if (mean) mean[r] = mu;
+        if (rstd) rstd[r] = rs;
+      }
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[k] = v[k] * rs * wr[k] + br[k];
+      Row::store(y + r * ys, d, v);
+    }
+  }
+}
+
+// dx, and the sums of dy hat and dy over the rows this workgroup walks over,
+// stored as slice blockIdx.x of the workspace (null: not needed): x and dy are
+// read once for all three gradients, the next row loaded ahead.  1024 threads have
+// 128 registers each, which hold the rows and weights but not the sums too
+// (they spilled): those rows keep their sums in LDS, 128 KB a workgroup, every
+// thread its own slots, and in fp32 load no row ahead.
+constexpr size_t norm_bwd_lds(int t) { return t > kNormThreads ? 2 * kNormElems * t * sizeof(float) : 0; }
+
+template <class Io, int T, bool RAGGED>
+__global__ void __launch_bounds__(norm_wg(T))
+    layer_norm_bwd_kernel(const typename Io::T* x, const float* w, const float* mean, const float* rstd,
+                          const typename Io::T* dy, typename Io::T* dx, float* ws, int64_t rows, int d, int64_t xs,
+                          int64_t dys, int64_t dxs) {
+  using Row = NormRow<Io, T, RAGGED>;
+  constexpr int WG = norm_wg(T), G = WG / T, E = Row::E;
+  __shared__ float s[2][2][WG / kWave];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  constexpr bool IN_LDS = T > kNormThreads, AHEAD = !IN_LDS || sizeof(typename Io::T) == 2;
+  FINETUNE_DYNAMIC_LDS(sums);  // IN_LDS: [2][E][T]
+  float* const mine = sums + threadIdx.x;
+  float wr[E], dw[IN_LDS ? 1 : E] = {}, db[IN_LDS ? 1 : E] = {};
+  if constexpr (IN_LDS)
+    for (int k = 0; k < 2 * E; ++k) mine[k * T] = 0.0f;
+  Row::params(w, d, 1.0f, wr);
+  const float n = static_cast<float>(d);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * G;
+  Row nx, ng;
+  float nm = 0.0f, nr = 0.0f;
+  int64_t r = first + threadIdx.x / T;
+  auto fetch = [&](int64_t row) {
+    nx.load(x + row * xs, d);
+    ng.load(dy + row * dys, d);
+    nm = mean[row];
+    nr = rstd[row];
+  };
+  if (AHEAD && r < rows) fetch(r);
+  int turn = 0;
+  for (int64_t r0 = first; r0 < rows; r0 += step, r += step, turn ^= 1) {
+    if (!AHEAD) fetch(r);  // one row a workgroup: r = r0
+    const Row cx = nx, cg = ng;
+    const float mu = nm, rs = nr;
+    if (AHEAD && r + step < rows) fetch(r + step);
+    const bool live = r < rows;
+    float a = 0.0f, c = 0.0f;
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const float g = cg.at(k), hat = (cx.at(k) - mu) * rs;
+      // columns past the row hold g = 0; a round without a row adds nothing
+      a += g * wr[k];
+      c += g * wr[k] * hat;
+      if constexpr (IN_LDS) {
+        mine[k * T] += g * hat;
+        mine[(E + k) * T] += g;
+      } else if (live) {
+        dw[k] += g * hat;
+        db[k] += g;
+      }
+    }
+    if (dx) {
+      a = group_sum<T>(a, s[turn][0]) / n;
+      c = group_sum<T>(c, s[turn][1]) / n;
+      if (live) {
+        float v[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          const float hat = (cx.at(k) - mu) * rs;
+          v[k] = rs * (cg.at(k) * wr[k] - a - hat * c);
+        }
+        Row::store(dx + r * dxs, d, v);
+      }
+    }
+  }
+  if (!ws) return;
+  float* slice = ws + static_cast<int64_t>(blockIdx.x) * 2 * d;
+  if constexpr (G > 1) {
+    // the groups' sums meet in LDS, in the order of the groups
+    __shared__ float join[G][T * E];
+    float* part[2] = {dw, db};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < E; ++k) join[threadIdx.x / T][Row::col(k / Row::V) + k % Row::V] = part[q][k];
+      __syncthreads();
+      for (int c = threadIdx.x; c < d; c += WG) {
+        float t = join[0][c];
+        for (int g = 1; g < G; ++g) t += join[g][c];
+        slice[q * d + c] = t;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const int c = Row::col(k / Row::V) + k % Row::V;
+      if (c < d) {
+        slice[c] = IN_LDS ? mine[k * T] : dw[IN_LDS ? 0 : k];
+        slice[d + c] = IN_LDS ? mine[(E + k) * T] : db[IN_LDS ? 0 : k];
+      }
+    }
+  }
+}
+
+// ---- rows of any length: one workgroup per row, the row read again for every
+// ---- sum (rows of more than 16384 elements, whose 64 KB stay in the caches)
+
+// The variance is the mean square of x - mean (a
 // second read of the row), not E x^2 - mean^2, which cancels for rows whose
 // mean is large against their spread.
 template <class Io>
 __global__ void __launch_bounds__(kNormThreads)
-    layer_norm_fwd_kernel(const typename Io::T* x, const float* w, const float* b, typename Io::T* y, float* mean,
+    layer_norm_wide_fwd_kernel(const typename Io::T* x, const float* w, const float* b, typename Io::T* y, float* mean,
                           float* rstd, int64_t rows, int d, int64_t xs, int64_t ys, float eps) {
   __shared__ float s[2][kNormThreads / kWave];
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
@@ -49,7 +273,7 @@ __global__ void __launch_bounds__(kNormThreads)
 // dx, one workgroup per row.
 template <class Io>
 __global__ void __launch_bounds__(kNormThreads)
-    layer_norm_dx_kernel(const typename Io::T* x, const float* w, const float* mean, const float* rstd,
+    layer_norm_wide_dx_kernel(const typename Io::T* x, const float* w, const float* mean, const float* rstd,
                          const typename Io::T* dy, typename Io::T* dx, int64_t rows, int d, int64_t xs, int64_t dys,
                          int64_t dxs) {
   __shared__ float s[2][kNormThreads / kWave];
@@ -76,7 +300,7 @@ __global__ void __launch_bounds__(kNormThreads)
 // [y * per, (y + 1) * per) go to slice y of the workspace.
 template <class Io>
 __global__ void __launch_bounds__(kNormThreads)
-    layer_norm_dw_kernel(const typename Io::T* x, const float* mean, const float* rstd, const typename Io::T* dy,
+    layer_norm_wide_dw_kernel(const typename Io::T* x, const float* mean, const float* rstd, const typename Io::T* dy,
                          float* ws, int64_t rows, int d, int64_t xs, int64_t dys, int64_t per) {
   const int j = blockIdx.x * kNormThreads + threadIdx.x;
   if (j >= d) return;
@@ -92,18 +316,25 @@ __global__ void __launch_bounds__(kNormThreads)
   slice[d + j] = a;
 }
 
-// The slices summed in order.
-__global__ void __launch_bounds__(kNormThreads)
+// ---- the sums over rows from the slices of the workspace, in order
+
+constexpr int kSumCols = 64;   // columns of a workgroup
+constexpr int kSumGroups = 16; // groups of slices summed side by side, then in order
+
+__global__ void __launch_bounds__(kSumCols* kSumGroups)
     layer_norm_dw_sum_kernel(const float* ws, float* dw, float* db, int d, int parts) {
-  const int j = blockIdx.x * kNormThreads + threadIdx.x;
-  if (j >= d) return;
-  float a = 0.0f, c = 0.0f;
-  for (int p = 0; p < parts; ++p) {
-    c += ws[static_cast<int64_t>(p) * 2 * d + j];
-    a += ws[static_cast<int64_t>(p) * 2 * d + d + j];
-  }
-  if (dw) dw[j] = c;
-  if (db) db[j] = a;
+  __shared__ float s[kSumGroups][kSumCols];
+  const int t = threadIdx.x % kSumCols, g = threadIdx.x / kSumCols;
+  const int c = blockIdx.x * kSumCols + t;  // dw's columns, then db's
+  float a = 0.0f;
+  if (c < 2 * d)
+    for (int p = g; p < parts; p += kSumGroups) a += ws[static_cast<int64_t>(p) * 2 * d + c];
+  s[g][t] = a;
+  __syncthreads();
+  if (g != 0 || c >= 2 * d) return;
+  for (int i = 1; i < kSumGroups; ++i) a += s[i][t];
+  float* o = c < d ? dw : db;
+  if (o) o[c < d ? c : c - d] = a;
 }
 
 }  // namespace finetune
