@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 // The workgroup's LDS block whose size the launch gives.  A host build that
 // runs the kernels on CPU threads defines it beforehand.
 #ifndef FINETUNE_DYNAMIC_LDS
@@ -45,22 +47,46 @@ struct F16 {
   }
 };
 
-// Sum of v over the workgroup (NT threads, a multiple of the wave), returned
-// to every thread; the order is fixed.  `s` holds NT / 64 slots and may be
-// reused after the next barrier.
-template <int NT, class V>
-__device__ __forceinline__ V block_sum(V v, V* s) {
-#pragma unroll
-  for (int o = kWave / 2; o > 0; o /= 2) v += __shfl_xor(v, o, kWave);
-  if constexpr (NT > kWave) {
-    const int w = threadIdx.x / kWave;
-    if (threadIdx.x % kWave == 0) s[w] = v;
-    __syncthreads();
-    v = s[0];
-#pragma unroll
-    for (int i = 1; i < NT / kWave; ++i) v += s[i];
+// Lane l's v from lane l ^ M of its wave, for M = 1, 2, or what serves in a sum
+// or maximum once the lanes below M agree: the mirrored lane of its 8 (M = 4)
+// or 16 (M = 8).  These move through the vector unit's data paths in a few
+// cycles; the general shuffle goes through LDS (norm_fwd_tokens 10.0 -> TBD us).
+template <int M>
+__device__ __forceinline__ uint32_t lane_swap(uint32_t v) {
+  constexpr int kCtrl = M == 1 ? 0xB1 : M == 2 ? 0x4E : M == 4 ? 0x141 : 0x140;
+  return __builtin_amdgcn_update_dpp(v, v, kCtrl, 0xf, 0xf, false);
+}
+
+// op over T consecutive lanes (T <= 64 a power of two), the result in all of
+// them.  op is commutative; the order of its application is fixed.
+template <int T, class F>
+__device__ __forceinline__ float lanes_reduce(float v, F op) {
+  auto f = [](uint32_t u) { return __builtin_bit_cast(float, u); };
+  auto u = [](float x) { return __builtin_bit_cast(uint32_t, x); };
+  if constexpr (T > 1) v = op(v, f(lane_swap<1>(u(v))));
+  if constexpr (T > 2) v = op(v, f(lane_swap<2>(u(v))));
+  if constexpr (T > 4) v = op(v, f(lane_swap<4>(u(v))));
+  if constexpr (T > 8) v = op(v, f(lane_swap<8>(u(v))));
+  if constexpr (T > 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(u(v), u(v), false, false);
+    v = op(f(p[0]), f(p[1]));
+  }
+  if constexpr (T > 32) {
+    const auto p = __builtin_amdgcn_permlane32_swap(u(v), u(v), false, false);
+    v = op(f(p[0]), f(p[1]));
   }
   return v;
+}
+
+template <int T, class V>
+__device__ __forceinline__ V lanes_sum(V v) {
+  if constexpr (std::is_same_v<V, float>) {
+    return lanes_reduce<T>(v, [](float a, float b) { return a + b; });
+  } else {
+#pragma unroll
+    for (int o = T / 2; o > 0; o /= 2) v += __shfl_xor(v, o, kWave);
+    return v;
+  }
 }
 
 // The sum over T consecutive threads of a workgroup of NT (T a power of two),
@@ -68,8 +94,7 @@ __device__ __forceinline__ V block_sum(V v, V* s) {
 // slots of `s` per group of T, which may be reused after the next barrier.
 template <int T, class V>
 __device__ __forceinline__ V group_sum(V v, V* s) {
-#pragma unroll
-  for (int o = (T < kWave ? T : kWave) / 2; o > 0; o /= 2) v += __shfl_xor(v, o, kWave);
+  v = lanes_sum<(T < kWave ? T : kWave)>(v);
   if constexpr (T > kWave) {
     constexpr int W = T / kWave;
     if (threadIdx.x % kWave == 0) s[threadIdx.x / kWave] = v;
@@ -80,6 +105,13 @@ __device__ __forceinline__ V group_sum(V v, V* s) {
     for (int i = 1; i < W; ++i) v += mine[i];
   }
   return v;
+}
+
+// Sum of v over the workgroup (NT threads, a multiple of the wave), returned
+// to every thread; `s` as above.
+template <int NT, class V>
+__device__ __forceinline__ V block_sum(V v, V* s) {
+  return group_sum<NT>(v, s);
 }
 
 }  // namespace finetune

@@ -318,8 +318,11 @@ __global__ void __launch_bounds__(kNormThreads)
 
 // ---- the sums over rows from the slices of the workspace, in order
 
-constexpr int kSumCols = 64;   // columns of a workgroup
-constexpr int kSumGroups = 16; // groups of slices summed side by side, then in order
+// 32 columns (one 128-byte line of a slice) by 32 groups of slices a workgroup:
+// 2 x 4096 columns fill the chip's 256 compute units, and a thread's few loads
+// are all in flight at once.
+constexpr int kSumCols = 32;
+constexpr int kSumGroups = 32;  // groups of slices summed side by side, then in order
 
 __global__ void __launch_bounds__(kSumCols* kSumGroups)
     layer_norm_dw_sum_kernel(const float* ws, float* dw, float* db, int d, int parts) {
@@ -327,8 +330,10 @@ __global__ void __launch_bounds__(kSumCols* kSumGroups)
   const int t = threadIdx.x % kSumCols, g = threadIdx.x / kSumCols;
   const int c = blockIdx.x * kSumCols + t;  // dw's columns, then db's
   float a = 0.0f;
-  if (c < 2 * d)
+  if (c < 2 * d) {
+#pragma unroll 8
     for (int p = g; p < parts; p += kSumGroups) a += ws[static_cast<int64_t>(p) * 2 * d + c];
+  }
   s[g][t] = a;
   __syncthreads();
   if (g != 0 || c >= 2 * d) return;
