@@ -50,7 +50,8 @@ struct F16 {
 // Lane l's v from lane l ^ M of its wave, for M = 1, 2, or what serves in a sum
 // or maximum once the lanes below M agree: the mirrored lane of its 8 (M = 4)
 // or 16 (M = 8).  These move through the vector unit's data paths in a few
-// cycles; the general shuffle goes through LDS (norm_fwd_tokens 10.0 -> TBD us).
+// cycles; the general shuffle goes through LDS (2048 x 4096 half layer norm 10.0 against 9.6 us,
+// one row of 4096 2.9 against 2.6 us).
 template <int M>
 __device__ __forceinline__ uint32_t lane_swap(uint32_t v) {
   constexpr int kCtrl = M == 1 ? 0xB1 : M == 2 ? 0x4E : M == 4 ? 0x141 : 0x140;

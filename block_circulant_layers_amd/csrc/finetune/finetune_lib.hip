@@ -136,13 +136,72 @@ Rows<Io> rows_of(const finetune_dlogits* out) {
   return {static_cast<typename Io::T*>(out->data), out->seq_stride, out->pos_stride};
 }
 
-int launch_logprob(const finetune_logits* in, float* logp, float* lse, hipStream_t s) {
+// How a launch over rows of `vocab` columns is split: `nt` threads a
+// workgroup, `parts` workgroups of `per` columns a row.  A row of up to four
+// pieces a lane takes one wave.  Fewer rows than kWantGroups workgroups are
+// split until there are as many, or until a part holds one piece a thread.
+constexpr int64_t kWantGroups = 1024;
+struct RowSplit {
+  int nt, parts, per;
+};
+RowSplit row_split(const finetune_logits* in) {
+  const int64_t v = in->vocab, piece = in->dtype == RDFFT_F32 ? 4 : 8;
+  RowSplit s{v <= 4 * kWave * piece ? kWave : kLogitThreads, 1, static_cast<int>(v)};
+  const int64_t rows = logit_rows(in);
+  if (rows > 0 && rows < kWantGroups && s.nt == kLogitThreads) {
+    const int64_t unit = s.nt * piece;
+    const int64_t parts = std::min<int64_t>(ceil_div(kWantGroups, rows), ceil_div(v, unit));
+    const int64_t per = ceil_div(ceil_div(v, parts), unit) * unit;
+    s.parts = static_cast<int>(ceil_div(v, per));
+    s.per = static_cast<int>(per);
+  }
+  return s;
+}
+
+template <class F>
+void by_threads(int nt, F f) {
+  if (nt == kWave)
+    f(std::integral_constant<int, kWave>{});
+  else
+    f(std::integral_constant<int, kLogitThreads>{});
+}
+
+// the parts of split rows: a maximum and a sum each
+int64_t logits_workspace(const finetune_logits* in) {
+  const RowSplit s = row_split(in);
+  return s.parts > 1 ? (logit_rows(in) * s.parts * 8 + 15) / 16 * 16 : 0;
+}
+
+template <class Io>
+JoinParts<Io> join_of(const finetune_logits* in, const RowSplit& split, float* lse, void* ws) {
+  return {rows_of<Io>(in), split.parts > 1 ? static_cast<const float2*>(ws) : nullptr, lse, split.parts,
+          static_cast<int>(in->vocab)};
+}
+
+// the rows' log-probabilities, or, where rows are split, their parts
+template <class Io>
+int launch_rows(const finetune_logits* in, const RowSplit& split, float* logp, float* lse, void* ws, hipStream_t s) {
   const int64_t rows = logit_rows(in);
   if (rows == 0) return RDFFT_OK;
+  by_threads(split.nt, [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    hipLaunchKernelGGL((token_logprob_kernel<Io, NT>), dim3(grid_of(rows * split.parts)), dim3(NT), 0, s,
+                       rows_of<Io>(in), in->labels, logp, lse, static_cast<float2*>(ws), rows, in->positions,
+                       static_cast<int>(in->vocab), split.parts, split.per);
+  });
+  return launch_status();
+}
+
+int launch_logprob(const finetune_logits* in, float* logp, float* lse, void* ws, hipStream_t s) {
   return by_dtype(in->dtype, [&](auto io) {
     using Io = decltype(io);
-    hipLaunchKernelGGL((token_logprob_kernel<Io>), dim3(grid_of(rows)), dim3(kLogitThreads), 0, s, rows_of<Io>(in),
-                       in->labels, logp, lse, rows, in->positions, static_cast<int>(in->vocab));
+    const RowSplit split = row_split(in);
+    const int st = launch_rows<Io>(in, split, logp, lse, ws, s);
+    if (st != RDFFT_OK || split.parts == 1) return st;
+    const int64_t rows = logit_rows(in);
+    hipLaunchKernelGGL((join_kernel<Io>), dim3(static_cast<unsigned>(ceil_div(rows, kLogitThreads))),
+                       dim3(kLogitThreads), 0, s, join_of<Io>(in, split, lse, ws), in->labels, logp, rows,
+                       in->positions);
     return launch_status();
   });
 }
@@ -153,42 +212,48 @@ int launch_grad(const finetune_logits* in, const float* lse, const RowScale& sca
   if (rows == 0) return RDFFT_OK;
   return by_dtype(in->dtype, [&](auto io) {
     using Io = decltype(io);
-    hipLaunchKernelGGL((logits_grad_kernel<Io>), dim3(grid_of(rows)), dim3(kLogitThreads), 0, s, rows_of<Io>(in),
-                       in->labels, lse, scale, rows_of<Io>(out), rows, in->positions, static_cast<int>(in->vocab));
+    const RowSplit split = row_split(in);
+    by_threads(split.nt, [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      hipLaunchKernelGGL((logits_grad_kernel<Io, NT>), dim3(grid_of(rows * split.parts)), dim3(NT), 0, s,
+                         rows_of<Io>(in), in->labels, lse, scale, rows_of<Io>(out), rows, in->positions,
+                         static_cast<int>(in->vocab), split.parts, split.per);
+    });
     return launch_status();
   });
 }
 
-int64_t logits_workspace(const finetune_logits* in) { return (in->seqs * 4 + 15) / 16 * 16; }  // counts
-
 int launch_preference(const finetune_logits* in, const float* ref, const finetune_preference* how, float* loss,
-                      float* logratio, float* logp, float* lse, float* slope, hipStream_t s) {
-  const int st = launch_logprob(in, logp, lse, s);
-  if (st != RDFFT_OK || in->seqs == 0) return st;
+                      float* logratio, float* logp, float* lse, float* slope, void* ws, hipStream_t s) {
+  if (in->seqs == 0) return RDFFT_OK;
   const Preference p{static_cast<int>(how->kind), how->average != 0, how->beta, how->smoothing};
   const int64_t pairs = in->seqs / 2;
-  hipLaunchKernelGGL((preference_kernel), dim3(grid_of(pairs)), dim3(kLogitThreads), 0, s, in->labels, logp, ref, p,
-                     loss, logratio, slope, pairs, in->positions);
-  return launch_status();
+  return by_dtype(in->dtype, [&](auto io) {
+    using Io = decltype(io);
+    const RowSplit split = row_split(in);
+    const int st = launch_rows<Io>(in, split, logp, lse, ws, s);
+    if (st != RDFFT_OK) return st;
+    hipLaunchKernelGGL((preference_kernel<Io>), dim3(grid_of(pairs)), dim3(kLogitThreads), 0, s,
+                       join_of<Io>(in, split, lse, ws), in->labels, logp, ref, p, loss, logratio, slope, pairs,
+                       in->positions);
+    return launch_status();
+  });
 }
 
 int launch_policy(const finetune_logits* in, const float* old, const float* ref, const float* adv,
                   const finetune_policy* how, float* stats, float* logp, float* lse, float* slope, void* ws,
                   hipStream_t s) {
-  int st = launch_logprob(in, logp, lse, s);
-  if (st != RDFFT_OK) return st;
-  auto* counts = static_cast<int*>(ws);
-  if (in->seqs > 0) {
-    hipLaunchKernelGGL((count_kernel), dim3(grid_of(in->seqs)), dim3(kLogitThreads), 0, s, in->labels, counts,
-                       in->seqs, in->positions);
-    st = launch_status();
-    if (st != RDFFT_OK) return st;
-  }
   const Policy p{static_cast<int>(how->reduction), how->advantage_per_token != 0, how->clip_low, how->clip_high,
                  how->kl_coef};
-  hipLaunchKernelGGL((policy_kernel), dim3(1), dim3(kLogitThreads), 0, s, in->labels, logp, old, ref, adv, counts, p,
-                     stats, slope, in->seqs, in->positions);
-  return launch_status();
+  return by_dtype(in->dtype, [&](auto io) {
+    using Io = decltype(io);
+    const RowSplit split = row_split(in);
+    const int st = launch_rows<Io>(in, split, logp, lse, ws, s);
+    if (st != RDFFT_OK) return st;
+    hipLaunchKernelGGL((policy_kernel<Io>), dim3(1), dim3(kPolicyThreads), 0, s, join_of<Io>(in, split, lse, ws),
+                       in->labels, logp, old, ref, adv, p, stats, slope, in->seqs, in->positions);
+    return launch_status();
+  });
 }
 
 // ---- gradient tensors -----------------------------------------------------
@@ -337,7 +402,7 @@ int token_logprob(const finetune_logits* in, float* logp, float* lse, void* ws, 
   const Array none[] = {{nullptr, 0}}, outs[] = {{logp, rows}, {lse, rows}};
   if (st == RDFFT_OK) st = check_arrays(in, nullptr, none, outs, ws, need);
   if (st != RDFFT_OK) return st;
-  return launch_logprob(in, logp, lse, static_cast<hipStream_t>(stream));
+  return launch_logprob(in, logp, lse, ws, static_cast<hipStream_t>(stream));
 }
 
 int token_logprob_bwd(const finetune_logits* in, const float* lse, const float* dlogp, const finetune_dlogits* out,
@@ -364,7 +429,7 @@ int preference_loss_fwd(const finetune_logits* in, const float* ref_logp, const 
   const Array outs[] = {{loss, in->seqs / 2}, {logratio, in->seqs}, {logp, rows}, {lse, rows}, {slope, in->seqs}};
   if (st == RDFFT_OK) st = check_arrays(in, nullptr, ins, outs, ws, need);
   if (st != RDFFT_OK) return st;
-  return launch_preference(in, ref_logp, how, loss, logratio, logp, lse, slope, static_cast<hipStream_t>(stream));
+  return launch_preference(in, ref_logp, how, loss, logratio, logp, lse, slope, ws, static_cast<hipStream_t>(stream));
 }
 
 int preference_loss_bwd(const finetune_logits* in, const float* lse, const float* slope, const float* dloss,
@@ -394,7 +459,7 @@ int preference_loss_step(const finetune_logits* in, const float* ref_logp, const
   if (st == RDFFT_OK) st = check_arrays(in, out, ins, outs, ws, need);
   if (st != RDFFT_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  st = launch_preference(in, ref_logp, how, loss, logratio, logp, lse, slope, s);
+  st = launch_preference(in, ref_logp, how, loss, logratio, logp, lse, slope, ws, s);
   if (st != RDFFT_OK) return st;
   return launch_grad(in, lse, RowScale{nullptr, slope, static_cast<float>(scale), 1, false}, out, s);
 }

@@ -14,81 +14,228 @@ constexpr int kLogitThreads = 256;
 constexpr int64_t kIgnore = -100;
 
 // Logits as the kernels see them: row r = (sequence r / positions, position
-// r % positions).
+// r % positions), both below 2^31.
 template <class Io>
 struct Rows {
   typename Io::T* data;
   int64_t seq_stride, pos_stride;
   __device__ __forceinline__ typename Io::T* row(int64_t r, int64_t positions) const {
-    return data + (r / positions) * seq_stride + (r % positions) * pos_stride;
+    const uint32_t n = static_cast<uint32_t>(positions), q = static_cast<uint32_t>(r) / n;
+    return data + q * seq_stride + (static_cast<uint32_t>(r) - q * n) * static_cast<int64_t>(pos_stride);
   }
 };
+
+constexpr float kLog2eHi = 1.44269502162933349609375f;
+constexpr float kLog2eLo = 1.925963033500011e-8f;  // log2(e) - kLog2eHi
 
 // exp(d) for d <= 0 through the hardware's exp2.  log2(e) is taken as a sum of
 // two floats: its rounding alone (1.3e-8) would shift every exponential, and
 // with it every log-probability, the same way, which a sum over a sequence's
 // positions does not average out.
 __device__ __forceinline__ float exp_of(float d) {
-  return __builtin_amdgcn_exp2f(__builtin_fmaf(d, 1.44269502162933349609375f, d * 1.925963033500011e-8f));
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(d, kLog2eHi, d * kLog2eLo));
 }
 
-// A running maximum and the sum of exp(x - maximum).
+__device__ __forceinline__ float max_of(float a, float b) { return a > b ? a : b; }
+
+// A running maximum m of values seen and s = the sum of exp(x - m); NaN values
+// make s NaN, values of -inf alone leave m = -inf and s = 0.
 struct MaxSum {
   float m = -INFINITY, s = 0.0f;
-  __device__ __forceinline__ void add(float x) {
-    if (x > m) {
-      s = s * exp_of(m - x) + 1.0f;
-      m = x;
-    } else {
-      s += x == m ? (m == -INFINITY ? 0.0f : 1.0f) : exp_of(x - m);
-    }
+  static __device__ __forceinline__ float base(float top) { return top == -INFINITY ? 0.0f : top; }
+  // n values at once: one rescaling for all of them
+  template <int N>
+  __device__ __forceinline__ void add(const float (&x)[N]) {
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = max_of(x[i], top);  // a NaN leaves top
+    const float b = base(top);
+    s *= exp_of(m - b);
+    m = top;
+    float a[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i % 2] += exp_of(x[i] - b);
+    s += a[0] + a[1];
   }
   __device__ __forceinline__ void join(float om, float os) {
-    const float top = m > om ? m : om;
-    if (top != m || top != om) {
-      s = s * (m == top ? 1.0f : exp_of(m - top)) + os * (om == top ? 1.0f : exp_of(om - top));
-      m = top;
-    } else {
-      s += os;
+    const float top = max_of(om, m), b = base(top);
+    s = s * exp_of(m - b) + os * exp_of(om - b);
+    m = top;
+  }
+  // over the NT threads of a workgroup, the result in every thread; `sm` holds
+  // 2 NT / 64 slots and may be reused after the next barrier
+  template <int NT>
+  __device__ __forceinline__ void join_group(float* sm) {
+    const float top = lanes_reduce<kWave>(m, [](float a, float b) { return max_of(a, b); });
+    s = lanes_sum<kWave>(s * exp_of(m - base(top)));
+    m = top;
+    if constexpr (NT > kWave) {
+      constexpr int W = NT / kWave;
+      if (threadIdx.x % kWave == 0) {
+        sm[threadIdx.x / kWave] = m;
+        sm[W + threadIdx.x / kWave] = s;
+      }
+      __syncthreads();
+      float all = sm[0];
+#pragma unroll
+      for (int i = 1; i < W; ++i) all = max_of(all, sm[i]);
+      const float b = base(all);
+      float t = 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) t += sm[W + i] * exp_of(sm[i] - b);
+      m = all;
+      s = t;
     }
   }
+  // log sum exp; NaN for a row whose maximum is infinite (its softmax has no value)
+  __device__ __forceinline__ double lse() const { return m + log(static_cast<double>(s)) + (m - m); }
 };
 
-// lse and logp of every position, one workgroup per row.
 template <class Io>
-__global__ void __launch_bounds__(kLogitThreads)
-    token_logprob_kernel(Rows<Io> in, const int64_t* labels, float* logp, float* lse, int64_t rows, int64_t positions,
-                         int v) {
-  __shared__ float sm[kLogitThreads / kWave], ss[kLogitThreads / kWave];
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+__device__ __forceinline__ typename Io::Vec load_vec(const typename Io::T* p) {
+  return *reinterpret_cast<const typename Io::Vec*>(p);
+}
+template <class Io>
+__device__ __forceinline__ void store_vec(typename Io::T* p, typename Io::Vec v) {
+  *reinterpret_cast<typename Io::Vec*>(p) = v;
+}
+
+// f(column) for the columns of [begin, end) that whole 16-byte pieces leave
+// over at the end, one a thread (fewer than 8)
+template <class Io, class F>
+__device__ __forceinline__ void for_rest(int begin, int end, F f) {
+  const int rest = (end - begin) % Io::kVec;
+  if (static_cast<int>(threadIdx.x) < rest) f(end - rest + static_cast<int>(threadIdx.x));
+}
+
+// Maximum and sum of the columns [begin, end) of a row by NT threads, four
+// 16-byte pieces of a thread in flight.
+template <class Io, int NT>
+__device__ __forceinline__ MaxSum row_max_sum(const typename Io::T* x, int begin, int end) {
+  constexpr int V = Io::kVec, U = 4;
+  MaxSum a;
+  int j = begin + static_cast<int>(threadIdx.x) * V;
+  for (; j + (U - 1) * NT * V + V <= end; j += U * NT * V) {
+    typename Io::Vec raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u] = load_vec<Io>(x + j + u * NT * V);
+    float f[U * V];
+#pragma unroll
+    for (int k = 0; k < U * V; ++k) f[k] = Io::widen(raw[k / V][k % V]);
+    a.add(f);
+  }
+  for (; j + V <= end; j += NT * V) {
+    const typename Io::Vec raw = load_vec<Io>(x + j);
+    float f[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = Io::widen(raw[k]);
+    a.add(f);
+  }
+  for_rest<Io>(begin, end, [&](int c) {
+    const float f[1] = {Io::widen(x[c])};
+    a.add(f);
+  });
+  return a;
+}
+
+// lse and logp of every position.  One workgroup per row (parts = 1), or, where
+// there are fewer rows than the chip has room for, `parts` workgroups of `per`
+// columns each, whose maxima and sums go to `partial` for the next kernel to
+// join.
+template <class Io, int NT>
+__global__ void __launch_bounds__(NT)
+    token_logprob_kernel(Rows<Io> in, const int64_t* labels, float* logp, float* lse, float2* partial, int64_t rows,
+                         int64_t positions, int v, int parts, int per) {
+  __shared__ float sm[2 * NT / kWave + 1];
+  for (int64_t i = blockIdx.x; i < rows * parts; i += gridDim.x) {
+    const int64_t r = parts == 1 ? i : static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(parts));
     const int64_t label = labels[r];
     if (label < 0 || label >= v) {
-      if (threadIdx.x == 0) logp[r] = lse[r] = label == kIgnore ? 0.0f : NAN;
+      if (parts == 1 && threadIdx.x == 0) logp[r] = lse[r] = label == kIgnore ? 0.0f : NAN;
       continue;
     }
     const typename Io::T* x = in.row(r, positions);
-    MaxSum a;
-    for (int j = threadIdx.x; j < v; j += kLogitThreads) a.add(Io::widen(x[j]));
-#pragma unroll
-    for (int o = kWave / 2; o > 0; o /= 2) a.join(__shfl_xor(a.m, o, kWave), __shfl_xor(a.s, o, kWave));
-    if (threadIdx.x % kWave == 0) {
-      sm[threadIdx.x / kWave] = a.m;
-      ss[threadIdx.x / kWave] = a.s;
-    }
-    __syncthreads();
+    const int begin = static_cast<int>(i - r * parts) * per, end = begin + per < v ? begin + per : v;
+    MaxSum a = row_max_sum<Io, NT>(x, begin, end);
+    a.template join_group<NT>(sm);
     if (threadIdx.x == 0) {
-      for (int i = 1; i < kLogitThreads / kWave; ++i) a.join(sm[i], ss[i]);
-      // a.m - a.m: NaN for a row whose maximum is infinite (its softmax has no value)
-      const double l = a.m + log(static_cast<double>(a.s)) + (a.m - a.m);
-      lse[r] = static_cast<float>(l);
-      logp[r] = static_cast<float>(Io::widen(x[label]) - l);
+      if (parts > 1) {
+        partial[i] = make_float2(a.m, a.s);
+      } else {
+        const double l = a.lse();
+        lse[r] = static_cast<float>(l);
+        logp[r] = static_cast<float>(Io::widen(x[label]) - l);
+      }
     }
-    __syncthreads();
+    if (NT > kWave) __syncthreads();
   }
 }
 
-// The gradient of every row: g = up[...] * slope[...], each either one value,
-// one per sequence (modulo `up_n`), or one per position.
+// The positions' lse and logp from their parts, one thread a row.
+template <class Io>
+struct JoinParts {
+  Rows<Io> in;
+  const float2* partial;  // null: logp and lse are there already
+  float* lse;
+  int parts, v;
+  // logp of row r (and, joined here, its lse stored)
+  __device__ __forceinline__ float operator()(int64_t r, int64_t label, int64_t positions, float* logp) const {
+    if (!partial) return logp[r];
+    double l = 0.0, p = 0.0;
+    if (label >= 0 && label < v) {
+      MaxSum a;
+      for (int i = 0; i < parts; ++i) {
+        const float2 q = partial[r * parts + i];
+        a.join(q.x, q.y);
+      }
+      l = a.lse();
+      p = Io::widen(in.row(r, positions)[label]) - l;
+    } else if (label != kIgnore) {
+      l = p = NAN;
+    }
+    lse[r] = static_cast<float>(l);
+    return logp[r] = static_cast<float>(p);
+  }
+};
+
+// ... for a caller that wants nothing but the log-probabilities
+template <class Io>
+__global__ void __launch_bounds__(kLogitThreads)
+    join_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, int64_t rows, int64_t positions) {
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * kLogitThreads + threadIdx.x;
+  if (r < rows) join(r, labels[r], positions, logp);
+}
+
+// One row's gradient g (1[j = label] - exp(x_j - lse)): with L = log2(e),
+// exp(x - lse) = exp2(x L - hi) exp2(-lo), where hi is lse L rounded and lo what
+// the rounding lost, so that one multiply-add and one exp2 an element suffice
+// and the second factor goes into g.
+struct RowGrad {
+  float g, scaled, hi;
+  int label;
+  __device__ __forceinline__ RowGrad(float g_, float lse, int label_) : g(g_), label(label_) {
+    hi = lse * kLog2eHi;
+    const float lo = __builtin_fmaf(lse, kLog2eHi, -hi) + lse * kLog2eLo;
+    scaled = -g * __builtin_amdgcn_exp2f(-lo);
+  }
+  __device__ __forceinline__ float at(float x) const {
+    return scaled * __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2eHi, -hi));
+  }
+  template <class Io>
+  __device__ __forceinline__ typename Io::Vec piece(typename Io::Vec x, int j) const {
+    typename Io::Vec o;
+#pragma unroll
+    for (int k = 0; k < Io::kVec; ++k) o[k] = Io::narrow(at(Io::widen(x[k])));
+    if (static_cast<unsigned>(label - j) < static_cast<unsigned>(Io::kVec)) {
+#pragma unroll
+      for (int k = 0; k < Io::kVec; ++k)
+        if (label == j + k) o[k] = Io::narrow(g + at(Io::widen(x[k])));
+    }
+    return o;
+  }
+};
+
+// The gradient's factor of every row: up[...] * slope[...].
 struct RowScale {
   const float* up;     // may be null (then `scale`)
   const float* slope;  // never null
@@ -96,30 +243,43 @@ struct RowScale {
   int64_t up_n;        // up is indexed by sequence modulo up_n
   bool slope_by_row;   // slope by row, else by sequence
   __device__ __forceinline__ float at(int64_t r, int64_t positions) const {
-    const int64_t seq = r / positions;
-    return (up ? up[seq % up_n] : scale) * slope[slope_by_row ? r : seq];
+    const uint32_t seq = static_cast<uint32_t>(r) / static_cast<uint32_t>(positions);
+    return (up ? up[seq % static_cast<uint32_t>(up_n)] : scale) * slope[slope_by_row ? r : seq];
   }
 };
 
-template <class Io>
-__global__ void __launch_bounds__(kLogitThreads)
+// The gradient of every row, `parts` workgroups of `per` columns a row.
+template <class Io, int NT>
+__global__ void __launch_bounds__(NT)
     logits_grad_kernel(Rows<Io> in, const int64_t* labels, const float* lse, RowScale scale, Rows<Io> out,
-                       int64_t rows, int64_t positions, int v) {
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+                       int64_t rows, int64_t positions, int v, int parts, int per) {
+  constexpr int V = Io::kVec, U = 4;
+  for (int64_t i = blockIdx.x; i < rows * parts; i += gridDim.x) {
+    const int64_t r = parts == 1 ? i : static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(parts));
+    const int begin = static_cast<int>(i - r * parts) * per, end = begin + per < v ? begin + per : v;
     const int64_t label = labels[r];
     typename Io::T* o = out.row(r, positions);
+    int j = begin + static_cast<int>(threadIdx.x) * V;
     if (label == kIgnore) {
-      for (int j = threadIdx.x; j < v; j += kLogitThreads) o[j] = Io::narrow(0.0f);
+      for (; j + V <= end; j += NT * V) store_vec<Io>(o + j, typename Io::Vec{});
+      for_rest<Io>(begin, end, [&](int c) { o[c] = 0; });
       continue;
     }
     const bool known = label >= 0 && label < v;
-    const float g = known ? scale.at(r, positions) : NAN;
-    const float l = lse[r];
+    const RowGrad grad(known ? scale.at(r, positions) : NAN, lse[r], known ? static_cast<int>(label) : -1);
     const typename Io::T* x = in.row(r, positions);
-    for (int j = threadIdx.x; j < v; j += kLogitThreads) {
-      const float p = exp_of(Io::widen(x[j]) - l);
-      o[j] = Io::narrow(g * ((j == label ? 1.0f : 0.0f) - p));
+    for (; j + (U - 1) * NT * V + V <= end; j += U * NT * V) {
+      typename Io::Vec raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u] = load_vec<Io>(x + j + u * NT * V);
+#pragma unroll
+      for (int u = 0; u < U; ++u) store_vec<Io>(o + j + u * NT * V, grad.piece<Io>(raw[u], j + u * NT * V));
     }
+    for (; j + V <= end; j += NT * V) store_vec<Io>(o + j, grad.piece<Io>(load_vec<Io>(x + j), j));
+    for_rest<Io>(begin, end, [&](int c) {
+      const float q = grad.at(Io::widen(x[c]));
+      o[c] = Io::narrow(c == grad.label ? grad.g + q : q);
+    });
   }
 }
 
@@ -131,9 +291,10 @@ struct Preference {
 
 // One workgroup per pair: both sequences' log-ratios, the loss and the slopes.
 // The sums run in fp64 (a few values per thread).
+template <class Io>
 __global__ void __launch_bounds__(kLogitThreads)
-    preference_kernel(const int64_t* labels, const float* logp, const float* ref, Preference how, float* loss,
-                      float* logratio, float* slope, int64_t pairs, int64_t positions) {
+    preference_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, const float* ref, Preference how,
+                      float* loss, float* logratio, float* slope, int64_t pairs, int64_t positions) {
   __shared__ double s[2][kLogitThreads / kWave];
   __shared__ double n[2][kLogitThreads / kWave];
   for (int64_t b = blockIdx.x; b < pairs; b += gridDim.x) {
@@ -142,11 +303,14 @@ __global__ void __launch_bounds__(kLogitThreads)
     for (int side = 0; side < 2; ++side) {
       const int64_t base = (b + side * pairs) * positions;
       double a = 0.0, c = 0.0;
-      for (int64_t i = threadIdx.x; i < positions; i += kLogitThreads)
-        if (labels[base + i] != kIgnore) {
-          a += static_cast<double>(logp[base + i]) - static_cast<double>(ref[base + i]);
+      for (int64_t i = threadIdx.x; i < positions; i += kLogitThreads) {
+        const int64_t label = labels[base + i];
+        const double p = join(base + i, label, positions, logp);
+        if (label != kIgnore) {
+          a += p - static_cast<double>(ref[base + i]);
           c += 1.0;
         }
+      }
       a = block_sum<kLogitThreads>(a, s[side]);
       c = block_sum<kLogitThreads>(c, n[side]);
       count[side] = how.average && c > 0.0 ? c : 1.0;
@@ -206,44 +370,47 @@ __device__ __forceinline__ PolicyTerm policy_term(const Policy& how, double logp
   return t;
 }
 
-// Unmasked positions of every sequence, one workgroup per sequence.
-__global__ void __launch_bounds__(kLogitThreads)
-    count_kernel(const int64_t* labels, int* counts, int64_t seqs, int64_t positions) {
-  __shared__ int s[kLogitThreads / kWave];
-  for (int64_t q = blockIdx.x; q < seqs; q += gridDim.x) {
-    int c = 0;
-    for (int64_t i = threadIdx.x; i < positions; i += kLogitThreads) c += labels[q * positions + i] != kIgnore;
-    c = block_sum<kLogitThreads>(c, s);
-    if (threadIdx.x == 0) counts[q] = c;
-    __syncthreads();
-  }
-}
+constexpr int kPolicyThreads = 1024;
 
-// Every position's slope and the reduced loss and KL: one workgroup.
-__global__ void __launch_bounds__(kLogitThreads)
-    policy_kernel(const int64_t* labels, const float* logp, const float* old, const float* ref, const float* adv,
-                  const int* counts, Policy how, float* stats, float* slope, int64_t seqs, int64_t positions) {
-  __shared__ double s[3][kLogitThreads / kWave];
+// Every position's slope and the reduced loss and KL: one workgroup, which also
+// joins the parts of split rows.  A wave takes a sequence at a time, so that
+// its count of unmasked positions stays within the wave.
+template <class Io>
+__global__ void __launch_bounds__(kPolicyThreads)
+    policy_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, const float* old, const float* ref,
+                  const float* adv, Policy how, float* stats, float* slope, int64_t seqs, int64_t positions) {
+  constexpr int W = kPolicyThreads / kWave;
+  __shared__ double s[3][W];
   double total = 0.0;
-  for (int64_t q = threadIdx.x; q < seqs; q += kLogitThreads) total += counts[q];
-  total = block_sum<kLogitThreads>(total, s[0]);
-  double a = 0.0, k = 0.0;
-  for (int64_t r = threadIdx.x; r < seqs * positions; r += kLogitThreads) {
-    float out = 0.0f;
-    if (labels[r] != kIgnore) {
-      const int64_t q = r / positions;
-      const double w = how.reduction == 0   ? 1.0 / total
-                       : how.reduction == 1 ? 1.0 / (static_cast<double>(counts[q]) * static_cast<double>(seqs))
-                                            : 1.0;
-      const PolicyTerm t = policy_term(how, logp[r], old[r], ref ? ref + r : nullptr, adv[how.per_token ? r : q]);
-      a += w * t.loss;
-      k += w * t.kl;
-      out = static_cast<float>(w * t.slope);
-    }
-    slope[r] = out;
+  if (how.reduction == 0) {
+    for (int64_t r = threadIdx.x; r < seqs * positions; r += kPolicyThreads) total += labels[r] != kIgnore;
+    total = block_sum<kPolicyThreads>(total, s[0]);
   }
-  a = block_sum<kLogitThreads>(a, s[1]);
-  k = block_sum<kLogitThreads>(k, s[2]);
+  const int lane = threadIdx.x % kWave;
+  double a = 0.0, k = 0.0;
+  for (int64_t q = threadIdx.x / kWave; q < seqs; q += W) {
+    const int64_t* lab = labels + q * positions;
+    double w = how.reduction == 0 ? 1.0 / total : 1.0;
+    if (how.reduction == 1) {
+      int c = 0;
+      for (int64_t i = lane; i < positions; i += kWave) c += lab[i] != kIgnore;
+      w = 1.0 / (static_cast<double>(lanes_sum<kWave>(c)) * static_cast<double>(seqs));
+    }
+    for (int64_t i = lane; i < positions; i += kWave) {
+      const int64_t r = q * positions + i;
+      const float p = join(r, lab[i], positions, logp);
+      float out = 0.0f;
+      if (lab[i] != kIgnore) {
+        const PolicyTerm t = policy_term(how, p, old[r], ref ? ref + r : nullptr, adv[how.per_token ? r : q]);
+        a += w * t.loss;
+        k += w * t.kl;
+        out = static_cast<float>(w * t.slope);
+      }
+      slope[r] = out;
+    }
+  }
+  a = block_sum<kPolicyThreads>(a, s[1]);
+  k = block_sum<kPolicyThreads>(k, s[2]);
   if (threadIdx.x == 0) {
     stats[0] = static_cast<float>(a);
     stats[1] = static_cast<float>(k);
