@@ -100,29 +100,27 @@ __device__ __forceinline__ void store_vec(typename Io::T* p, typename Io::Vec v)
   *reinterpret_cast<typename Io::Vec*>(p) = v;
 }
 
-// The columns [begin, end) of a row as 16-byte pieces at addresses divisible
-// by 16 (rows start at any element): `first` columns before them, the pieces up
-// to `last`, and what is left.  Pieces at other addresses straddle cache lines:
-// reading 5300 rows of 50001 bf16 took 170 us so, 148 us in aligned pieces, and
-// their gradient 281 against 260 us.
+// The columns [begin, end) of a row (rows start at any element): 16-byte pieces
+// from the first 128-byte line on, up to `last`, and the columns before and
+// after them.  Pieces at odd addresses straddle lines: reading 5808 rows of
+// 50001 bf16 took 170 us from the row's start, 148 us from the first address
+// divisible by 16, and 141 us from the first line on (their gradient: 281, 260,
+// 248 us).
 template <class Io>
 struct Pieces {
   int begin, first, last, end;
   __device__ __forceinline__ Pieces(const typename Io::T* row, int b, int e) : begin(b), end(e) {
-    constexpr int V = Io::kVec, S = sizeof(typename Io::T);
-    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row + b) / S % V);
-    first = b + (V - off) % V;
+    constexpr int S = sizeof(typename Io::T), L = 128 / S;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row + b) / S % L);
+    first = b + (L - off) % L;
     if (first > e) first = e;
-    last = first + (e - first) / V * V;
+    last = first + (e - first) / Io::kVec * Io::kVec;
   }
-  // f(column) for the columns outside the pieces, at most one a thread
-  template <class F>
+  // f(column) for the columns outside the pieces
+  template <int NT, class F>
   __device__ __forceinline__ void rest(F f) const {
-    const int t = static_cast<int>(threadIdx.x), head = first - begin;
-    if (t < head)
-      f(begin + t);
-    else if (t - head < end - last)
-      f(last + t - head);
+    const int head = first - begin, n = head + end - last;
+    for (int t = threadIdx.x; t < n; t += NT) f(t < head ? begin + t : last + t - head);
   }
 };
 
@@ -150,7 +148,7 @@ __device__ __forceinline__ MaxSum row_max_sum(const typename Io::T* x, int begin
     for (int k = 0; k < V; ++k) f[k] = Io::widen(raw[k]);
     a.add(f);
   }
-  p.rest([&](int c) {
+  p.template rest<NT>([&](int c) {
     const float f[1] = {Io::widen(x[c])};
     a.add(f);
   });
@@ -282,7 +280,7 @@ __global__ void __launch_bounds__(NT)
       const Pieces<Io> p(o, begin, end);
       for (int j = p.first + static_cast<int>(threadIdx.x) * V; j < p.last; j += NT * V)
         store_vec<Io>(o + j, typename Io::Vec{});
-      p.rest([&](int c) { o[c] = 0; });
+      p.template rest<NT>([&](int c) { o[c] = 0; });
       continue;
     }
     const bool known = label >= 0 && label < v;
@@ -298,7 +296,7 @@ __global__ void __launch_bounds__(NT)
       for (int u = 0; u < U; ++u) store_vec<Io>(o + j + u * NT * V, grad.piece<Io>(raw[u], j + u * NT * V));
     }
     for (; j < p.last; j += NT * V) store_vec<Io>(o + j, grad.piece<Io>(load_vec<Io>(x + j), j));
-    p.rest([&](int c) {
+    p.template rest<NT>([&](int c) {
       const float q = grad.at(Io::widen(x[c]));
       o[c] = Io::narrow(c == grad.label ? grad.g + q : q);
     });
