@@ -12,6 +12,15 @@
 #define FINETUNE_DYNAMIC_LDS(name) extern __shared__ float name[]
 #endif
 
+// Two pieces of gfx950 assembly, which a host build defines otherwise: the
+// maximum of three values (the compiler's fmaxf first quiets every operand;
+// a NaN is ignored or returned), and a value the compiler must not trace back,
+// so that it does not keep in registers what is cheap to compute again.
+#ifndef FINETUNE_MAX3
+#define FINETUNE_MAX3(out, a, b, c) asm("v_max3_f32 %0, %1, %2, %3" : "=v"(out) : "v"(a), "v"(b), "v"(c))
+#define FINETUNE_OPAQUE(x) asm volatile("" : "+v"(x))
+#endif
+
 namespace finetune {
 
 constexpr int kWave = 64;

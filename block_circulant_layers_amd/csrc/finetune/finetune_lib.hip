@@ -166,15 +166,29 @@ void by_threads(int nt, F f) {
     f(std::integral_constant<int, kLogitThreads>{});
 }
 
-// the parts of split rows: a maximum and a sum each
-int64_t logits_workspace(const finetune_logits* in) {
-  const RowSplit s = row_split(in);
-  return s.parts > 1 ? (logit_rows(in) * s.parts * 8 + 15) / 16 * 16 : 0;
+// Workspace of the calls on logits: one total, a count a sequence, two fp64
+// shares a row (policy loss), and the parts of split rows (a maximum and a sum
+// each).
+struct LogitsWorkspace {
+  int64_t counts, terms, parts, bytes;  // offsets, and the size
+  explicit LogitsWorkspace(const finetune_logits* in) {
+    const auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
+    const RowSplit s = row_split(in);
+    counts = 16;
+    terms = counts + up(in->seqs * 4);
+    parts = terms + logit_rows(in) * 16;
+    bytes = parts + (s.parts > 1 ? up(logit_rows(in) * s.parts * 8) : 0);
+  }
+};
+int64_t logits_workspace(const finetune_logits* in) { return LogitsWorkspace(in).bytes; }
+template <class T>
+T* at(void* ws, int64_t offset) {
+  return reinterpret_cast<T*>(static_cast<char*>(ws) + offset);
 }
 
 template <class Io>
 JoinParts<Io> join_of(const finetune_logits* in, const RowSplit& split, float* lse, void* ws) {
-  return {rows_of<Io>(in), split.parts > 1 ? static_cast<const float2*>(ws) : nullptr, lse, split.parts,
+  return {rows_of<Io>(in), split.parts > 1 ? at<const float2>(ws, LogitsWorkspace(in).parts) : nullptr, lse, split.parts,
           static_cast<int>(in->vocab)};
 }
 
@@ -186,7 +200,7 @@ int launch_rows(const finetune_logits* in, const RowSplit& split, float* logp, f
   by_threads(split.nt, [&](auto nt) {
     constexpr int NT = decltype(nt)::value;
     hipLaunchKernelGGL((token_logprob_kernel<Io, NT>), dim3(grid_of(rows * split.parts)), dim3(NT), 0, s,
-                       rows_of<Io>(in), in->labels, logp, lse, static_cast<float2*>(ws), rows, in->positions,
+                       rows_of<Io>(in), in->labels, logp, lse, at<float2>(ws, LogitsWorkspace(in).parts), rows, in->positions,
                        static_cast<int>(in->vocab), split.parts, split.per);
   });
   return launch_status();
@@ -240,20 +254,108 @@ int launch_preference(const finetune_logits* in, const float* ref, const finetun
   });
 }
 
-int launch_policy(const finetune_logits* in, const float* old, const float* ref, const float* adv,
-                  const finetune_policy* how, float* stats, float* logp, float* lse, float* slope, void* ws,
-                  hipStream_t s) {
-  const Policy p{static_cast<int>(how->reduction), how->advantage_per_token != 0, how->clip_low, how->clip_high,
-                 how->kl_coef};
+// Rows up to which one workgroup does all that follows the log-probabilities
+// (8192 rows took it TBD us, three launches TBD us).
+constexpr int64_t kPolicyOne = 2048;
+
+// what policy kernels share
+struct PolicyCall {
+  Policy how;
+  PolicyInputs in;
+  PolicyWeight weight;
+  int *counts, *total;
+  double2* terms;
+};
+PolicyCall policy_call(const finetune_logits* in, const float* old, const float* ref, const float* adv,
+                       const finetune_policy* how, void* ws) {
+  const LogitsWorkspace w(in);
+  const int reduction = static_cast<int>(how->reduction);
+  int *counts = at<int>(ws, w.counts), *total = at<int>(ws, 0);
+  return {{reduction, how->clip_low, how->clip_high, how->kl_coef},
+          {old, ref, adv, how->advantage_per_token != 0},
+          {counts, total, reduction, in->seqs},
+          counts,
+          total,
+          at<double2>(ws, w.terms)};
+}
+
+int launch_policy_count(const finetune_logits* in, const PolicyCall& c, hipStream_t s) {
+  if (c.how.reduction == POLICY_SUM) return RDFFT_OK;
+  hipLaunchKernelGGL((policy_count_kernel), dim3(1), dim3(kPolicyThreads), 0, s, in->labels, c.counts, c.total,
+                     c.how.reduction, in->seqs, in->positions);
+  return launch_status();
+}
+
+int launch_policy_sum(const finetune_logits* in, const PolicyCall& c, float* stats, hipStream_t s) {
+  hipLaunchKernelGGL((policy_sum_kernel), dim3(1), dim3(kPolicyThreads), 0, s, c.terms, stats, logit_rows(in));
+  return launch_status();
+}
+
+int launch_policy(const finetune_logits* in, const PolicyCall& c, float* stats, float* logp, float* lse, float* slope,
+                  void* ws, hipStream_t s) {
   return by_dtype(in->dtype, [&](auto io) {
     using Io = decltype(io);
     const RowSplit split = row_split(in);
-    const int st = launch_rows<Io>(in, split, logp, lse, ws, s);
+    const int64_t rows = logit_rows(in);
+    int st = launch_rows<Io>(in, split, logp, lse, ws, s);
     if (st != RDFFT_OK) return st;
-    hipLaunchKernelGGL((policy_kernel<Io>), dim3(1), dim3(kPolicyThreads), 0, s, join_of<Io>(in, split, lse, ws),
-                       in->labels, logp, old, ref, adv, p, stats, slope, in->seqs, in->positions);
+    if (rows <= kPolicyOne) {
+      hipLaunchKernelGGL((policy_kernel<Io, true>), dim3(1), dim3(kPolicyThreads), 0, s,
+                         join_of<Io>(in, split, lse, ws), in->labels, logp, c.in, c.weight, c.counts, c.total, c.how,
+                         stats, slope, c.terms, in->seqs, in->positions);
+      return launch_status();
+    }
+    st = launch_policy_count(in, c, s);
+    if (st != RDFFT_OK) return st;
+    hipLaunchKernelGGL((policy_kernel<Io, false>), dim3(grid_of(ceil_div(rows, kLogitThreads))), dim3(kLogitThreads),
+                       0, s, join_of<Io>(in, split, lse, ws), in->labels, logp, c.in, c.weight, c.counts, c.total,
+                       c.how, stats, slope, c.terms, in->seqs, in->positions);
+    st = launch_status();
+    return st == RDFFT_OK ? launch_policy_sum(in, c, stats, s) : st;
+  });
+}
+
+// The step with the rows held in registers, where there are rows enough to fill
+// the chip and a row fits a workgroup: f(threads, pieces a thread), and whether
+// there was such a shape.
+template <class F>
+bool by_held_row(const finetune_logits* in, F f) {
+  const int64_t pieces = in->vocab / (in->dtype == RDFFT_F32 ? 4 : 8);
+  if (logit_rows(in) < kWantGroups) return false;
+  if (pieces <= 64 * 8)
+    f(std::integral_constant<int, 64>{}, std::integral_constant<int, 8>{});
+  else if (pieces <= 256 * 8)
+    f(std::integral_constant<int, 256>{}, std::integral_constant<int, 8>{});
+  else if (pieces <= 512 * 16)
+    f(std::integral_constant<int, 512>{}, std::integral_constant<int, 16>{});
+  else if (pieces <= 1024 * 16)
+    f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 16>{});
+  else
+    return false;
+  return true;
+}
+
+int launch_policy_step(const finetune_logits* in, const PolicyCall& c, float scale, float* stats, float* logp,
+                       float* lse, float* slope, const finetune_dlogits* out, void* ws, hipStream_t s) {
+  const bool held = by_held_row(in, [](auto, auto) {});
+  if (!held) {
+    const int st = launch_policy(in, c, stats, logp, lse, slope, ws, s);
+    if (st != RDFFT_OK) return st;
+    return launch_grad(in, lse, RowScale{nullptr, slope, scale, 1, true}, out, s);
+  }
+  int st = launch_policy_count(in, c, s);
+  if (st != RDFFT_OK) return st;
+  st = by_dtype(in->dtype, [&](auto io) {
+    using Io = decltype(io);
+    by_held_row(in, [&](auto nt, auto r) {
+      constexpr int NT = decltype(nt)::value, R = decltype(r)::value;
+      hipLaunchKernelGGL((policy_step_kernel<Io, NT, R>), dim3(static_cast<unsigned>(logit_rows(in))), dim3(NT), 0, s,
+                         rows_of<Io>(in), in->labels, c.in, c.weight, c.how, scale, logp, lse, slope, c.terms,
+                         rows_of<Io>(out), in->positions, static_cast<int>(in->vocab));
+    });
     return launch_status();
   });
+  return st == RDFFT_OK ? launch_policy_sum(in, c, stats, s) : st;
 }
 
 // ---- gradient tensors -----------------------------------------------------
@@ -476,7 +578,7 @@ int policy_loss_fwd(const finetune_logits* in, const float* old_logp, const floa
   const Array outs[] = {{stats, 2}, {logp, rows}, {lse, rows}, {slope, rows}};
   if (st == RDFFT_OK) st = check_arrays(in, nullptr, ins, outs, ws, need);
   if (st != RDFFT_OK) return st;
-  return launch_policy(in, old_logp, ref_logp, advantages, how, stats, logp, lse, slope, ws,
+  return launch_policy(in, policy_call(in, old_logp, ref_logp, advantages, how, ws), stats, logp, lse, slope, ws,
                        static_cast<hipStream_t>(stream));
 }
 
@@ -505,10 +607,8 @@ int policy_loss_step(const finetune_logits* in, const float* old_logp, const flo
   const Array outs[] = {{stats, 2}, {logp, rows}, {lse, rows}, {slope, rows}};
   if (st == RDFFT_OK) st = check_arrays(in, out, ins, outs, ws, need);
   if (st != RDFFT_OK) return st;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  st = launch_policy(in, old_logp, ref_logp, advantages, how, stats, logp, lse, slope, ws, s);
-  if (st != RDFFT_OK) return st;
-  return launch_grad(in, lse, RowScale{nullptr, slope, static_cast<float>(scale), 1, true}, out, s);
+  return launch_policy_step(in, policy_call(in, old_logp, ref_logp, advantages, how, ws), static_cast<float>(scale),
+                            stats, logp, lse, slope, out, ws, static_cast<hipStream_t>(stream));
 }
 
 int grad_norm_workspace(const finetune_tensor* tensors, int64_t n, int64_t* bytes) {

@@ -38,6 +38,16 @@ __device__ __forceinline__ float exp_of(float d) {
 
 __device__ __forceinline__ float max_of(float a, float b) { return a > b ? a : b; }
 
+// the largest of n values and `top`, n even
+template <int N>
+__device__ __forceinline__ float max_over(const float (&x)[N], float top) {
+  static_assert(N % 2 == 0);
+  float a[2] = {top, top};
+#pragma unroll
+  for (int i = 0; i < N; i += 2) FINETUNE_MAX3(a[i / 2 % 2], x[i], x[i + 1], a[i / 2 % 2]);
+  return max_of(a[0], a[1]);
+}
+
 // A running maximum m of values seen and s = the sum of exp(x - m); NaN values
 // make s NaN, values of -inf alone leave m = -inf and s = 0.
 struct MaxSum {
@@ -46,9 +56,7 @@ struct MaxSum {
   // n values at once: one rescaling for all of them
   template <int N>
   __device__ __forceinline__ void add(const float (&x)[N]) {
-    float top = m;
-#pragma unroll
-    for (int i = 0; i < N; ++i) top = max_of(x[i], top);  // a NaN leaves top
+    const float top = max_over(x, m);
     const float b = base(top);
     s *= exp_of(m - b);
     m = top;
@@ -106,11 +114,11 @@ __device__ __forceinline__ void store_vec(typename Io::T* p, typename Io::Vec v)
 // 50001 bf16 took 170 us from the row's start, 148 us from the first address
 // divisible by 16, and 141 us from the first line on (their gradient: 281, 260,
 // 248 us).
-template <class Io>
+template <class Io, int LINE = 128>
 struct Pieces {
   int begin, first, last, end;
   __device__ __forceinline__ Pieces(const typename Io::T* row, int b, int e) : begin(b), end(e) {
-    constexpr int S = sizeof(typename Io::T), L = 128 / S;
+    constexpr int S = sizeof(typename Io::T), L = LINE / S;
     const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row + b) / S % L);
     first = b + (L - off) % L;
     if (first > e) first = e;
@@ -149,7 +157,7 @@ __device__ __forceinline__ MaxSum row_max_sum(const typename Io::T* x, int begin
     a.add(f);
   }
   p.template rest<NT>([&](int c) {
-    const float f[1] = {Io::widen(x[c])};
+    const float f[2] = {Io::widen(x[c]), -INFINITY};
     a.add(f);
   });
   return a;
@@ -364,7 +372,6 @@ __global__ void __launch_bounds__(kLogitThreads)
 
 struct Policy {
   int reduction;
-  bool per_token;
   double low, high, kl;
 };
 
@@ -390,50 +397,223 @@ __device__ __forceinline__ PolicyTerm policy_term(const Policy& how, double logp
   return t;
 }
 
+// What a position counts in the reduced loss.
+struct PolicyWeight {
+  const int* counts;  // unmasked positions of every sequence (POLICY_SEQUENCE_MEAN)
+  const int* total;   // ... of all (POLICY_TOKEN_MEAN)
+  int reduction;
+  int64_t seqs;
+  __device__ __forceinline__ double at(int64_t seq) const {
+    if (reduction == 0) return 1.0 / static_cast<double>(total[0]);
+    if (reduction == 1) return 1.0 / (static_cast<double>(counts[seq]) * static_cast<double>(seqs));
+    return 1.0;
+  }
+};
+
+struct PolicyInputs {
+  const float *old, *ref, *adv;  // ref may be null
+  bool per_token;
+};
+
 constexpr int kPolicyThreads = 1024;
 
-// Every position's slope and the reduced loss and KL: one workgroup, which also
-// joins the parts of split rows.  A wave takes a sequence at a time, so that
-// its count of unmasked positions stays within the wave.
-template <class Io>
-__global__ void __launch_bounds__(kPolicyThreads)
-    policy_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, const float* old, const float* ref,
-                  const float* adv, Policy how, float* stats, float* slope, int64_t seqs, int64_t positions) {
-  constexpr int W = kPolicyThreads / kWave;
-  __shared__ double s[3][W];
-  double total = 0.0;
-  if (how.reduction == 0) {
-    for (int64_t r = threadIdx.x; r < seqs * positions; r += kPolicyThreads) total += labels[r] != kIgnore;
-    total = block_sum<kPolicyThreads>(total, s[0]);
-  }
-  const int lane = threadIdx.x % kWave;
-  double a = 0.0, k = 0.0;
-  for (int64_t q = threadIdx.x / kWave; q < seqs; q += W) {
-    const int64_t* lab = labels + q * positions;
-    double w = how.reduction == 0 ? 1.0 / total : 1.0;
-    if (how.reduction == 1) {
+// The counts that the reduction needs, by one workgroup: all positions at once,
+// or a wave for a sequence at a time.
+__device__ __forceinline__ void policy_counts(const int64_t* labels, int* counts, int* total, int reduction,
+                                              int64_t seqs, int64_t positions, int* s) {
+  if (reduction == 0) {
+    int c = 0;
+#pragma unroll 8
+    for (int64_t r = threadIdx.x; r < seqs * positions; r += kPolicyThreads) c += labels[r] != kIgnore;
+    c = block_sum<kPolicyThreads>(c, s);
+    if (threadIdx.x == 0) total[0] = c;
+  } else if (reduction == 1) {
+    const int lane = threadIdx.x % kWave;
+    for (int64_t q = threadIdx.x / kWave; q < seqs; q += kPolicyThreads / kWave) {
       int c = 0;
-      for (int64_t i = lane; i < positions; i += kWave) c += lab[i] != kIgnore;
-      w = 1.0 / (static_cast<double>(lanes_sum<kWave>(c)) * static_cast<double>(seqs));
-    }
-    for (int64_t i = lane; i < positions; i += kWave) {
-      const int64_t r = q * positions + i;
-      const float p = join(r, lab[i], positions, logp);
-      float out = 0.0f;
-      if (lab[i] != kIgnore) {
-        const PolicyTerm t = policy_term(how, p, old[r], ref ? ref + r : nullptr, adv[how.per_token ? r : q]);
-        a += w * t.loss;
-        k += w * t.kl;
-        out = static_cast<float>(w * t.slope);
-      }
-      slope[r] = out;
+#pragma unroll 8
+      for (int64_t i = lane; i < positions; i += kWave) c += labels[q * positions + i] != kIgnore;
+      c = lanes_sum<kWave>(c);
+      if (lane == 0) counts[q] = c;
     }
   }
-  a = block_sum<kPolicyThreads>(a, s[1]);
-  k = block_sum<kPolicyThreads>(k, s[2]);
+}
+
+__global__ void __launch_bounds__(kPolicyThreads)
+    policy_count_kernel(const int64_t* labels, int* counts, int* total, int reduction, int64_t seqs,
+                        int64_t positions) {
+  __shared__ int s[kPolicyThreads / kWave];
+  policy_counts(labels, counts, total, reduction, seqs, positions, s);
+}
+
+// One position's slope (stored) and its share of the loss and the KL.
+__device__ __forceinline__ double2 policy_row(const Policy& how, const PolicyInputs& in, double weight, int64_t r,
+                                              int64_t seq, float logp, float* slope) {
+  const PolicyTerm t =
+      policy_term(how, logp, in.old[r], in.ref ? in.ref + r : nullptr, in.adv[in.per_token ? r : seq]);
+  slope[r] = static_cast<float>(weight * t.slope);
+  return make_double2(weight * t.loss, weight * t.kl);
+}
+
+// Every position's slope, and the reduced loss and KL.  ONE: everything in one
+// workgroup, the counts too; else a thread a row, whose shares go to `terms`
+// for policy_sum_kernel, after policy_count_kernel.
+template <class Io, bool ONE>
+__global__ void __launch_bounds__(ONE ? kPolicyThreads : kLogitThreads)
+    policy_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, PolicyInputs in, PolicyWeight weight,
+                  int* counts, int* total, Policy how, float* stats, float* slope, double2* terms, int64_t seqs,
+                  int64_t positions) {
+  constexpr int NT = ONE ? kPolicyThreads : kLogitThreads;
+  __shared__ double s[2][NT / kWave];
+  __shared__ int sc[NT / kWave];
+  if constexpr (ONE) {
+    policy_counts(labels, counts, total, how.reduction, seqs, positions, sc);
+    __syncthreads();
+  }
+  const uint32_t rows = static_cast<uint32_t>(seqs * positions), n = static_cast<uint32_t>(positions);
+  double a = 0.0, k = 0.0;
+  for (uint32_t r = blockIdx.x * NT + threadIdx.x; r < rows; r += gridDim.x * NT) {
+    const int64_t label = labels[r];
+    const float p = join(r, label, positions, logp);
+    double2 t = make_double2(0.0, 0.0);
+    if (label != kIgnore)
+      t = policy_row(how, in, weight.at(r / n), r, r / n, p, slope);
+    else
+      slope[r] = 0.0f;
+    if (ONE) {
+      a += t.x;
+      k += t.y;
+    } else {
+      terms[r] = t;
+    }
+  }
+  if constexpr (ONE) {
+    a = block_sum<NT>(a, s[0]);
+    k = block_sum<NT>(k, s[1]);
+    if (threadIdx.x == 0) {
+      stats[0] = static_cast<float>(a);
+      stats[1] = static_cast<float>(k);
+    }
+  }
+}
+
+// The positions' shares summed in a fixed order.
+__global__ void __launch_bounds__(kPolicyThreads)
+    policy_sum_kernel(const double2* terms, float* stats, int64_t rows) {
+  __shared__ double s[2][kPolicyThreads / kWave];
+  double a = 0.0, k = 0.0;
+#pragma unroll 8
+  for (int64_t r = threadIdx.x; r < rows; r += kPolicyThreads) {
+    const double2 t = terms[r];
+    a += t.x;
+    k += t.y;
+  }
+  a = block_sum<kPolicyThreads>(a, s[0]);
+  k = block_sum<kPolicyThreads>(k, s[1]);
   if (threadIdx.x == 0) {
     stats[0] = static_cast<float>(a);
     stats[1] = static_cast<float>(k);
+  }
+}
+
+// A position's log-probability, loss share, slope and gradient with its logits
+// read once: one workgroup holds the row in registers, R 16-byte pieces a
+// thread (pieces past the row hold -inf, which adds nothing), and one more
+// column a thread for what lies outside the pieces.
+template <class Io>
+__device__ __forceinline__ typename Io::Vec lowest_vec() {
+  typename Io::Vec v;
+#pragma unroll
+  for (int k = 0; k < Io::kVec; ++k) v[k] = Io::narrow(-INFINITY);
+  return v;
+}
+
+template <class Io, int NT, int R>
+__global__ void __launch_bounds__(NT, 4)  // 128 registers: 16 waves a compute unit
+    policy_step_kernel(Rows<Io> in, const int64_t* labels, PolicyInputs inputs, PolicyWeight weight, Policy how,
+                       float scale, float* logp, float* lse, float* slope, double2* terms, Rows<Io> out,
+                       int64_t positions, int v) {
+  constexpr int V = Io::kVec;
+  __shared__ float sm[2 * NT / kWave];
+  __shared__ float told[2];
+  const int64_t r = blockIdx.x;
+  const int64_t label = labels[r];
+  typename Io::T* o = out.row(r, positions);
+  if (label < 0 || label >= v) {
+    // masked: zeros; a label out of range: NaN
+    const float fill = label == kIgnore ? 0.0f : NAN;
+    typename Io::Vec f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = Io::narrow(fill);
+    const Pieces<Io> p(o, 0, v);
+    for (int j = p.first + static_cast<int>(threadIdx.x) * V; j < p.last; j += NT * V) store_vec<Io>(o + j, f);
+    p.template rest<NT>([&](int c) { o[c] = f[0]; });
+    if (threadIdx.x == 0) {
+      logp[r] = lse[r] = slope[r] = fill;
+      terms[r] = make_double2(fill, fill);
+    }
+    return;
+  }
+  const typename Io::T* x = in.row(r, positions);
+  const Pieces<Io, NT == kWave ? 16 : 128> p(o, 0, v);  // at most NT columns outside the pieces
+  typename Io::Vec raw[R];
+  int j = p.first + static_cast<int>(threadIdx.x) * V;
+#pragma unroll
+  for (int i = 0; i < R; ++i) raw[i] = j + i * NT * V < p.last ? load_vec<Io>(x + j + i * NT * V) : lowest_vec<Io>();
+  int column = -1;
+  p.template rest<NT>([&](int c) { column = c; });
+  const float extra = column >= 0 ? Io::widen(x[column]) : -INFINITY;
+  const float picked = threadIdx.x == 0 ? Io::widen(x[label]) : 0.0f;
+
+  const auto widened = [&](int i, float (&f)[V]) {
+    // opaque: the widened values are recomputed at each use, the registers hold the stored ones
+    typedef uint32_t Words __attribute__((ext_vector_type(4)));
+    Words w = __builtin_bit_cast(Words, raw[i]);
+    FINETUNE_OPAQUE(w);
+    raw[i] = __builtin_bit_cast(typename Io::Vec, w);
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = Io::widen(raw[i][k]);
+  };
+  float top = extra;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    float f[V];
+    widened(i, f);
+    top = max_over(f, top);
+  }
+  MaxSum a;
+  a.m = top;
+  const float b = MaxSum::base(top);
+  float t[2] = {exp_of(extra - b), 0.0f};
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    float f[V];
+    widened(i, f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) t[k % 2] += exp_of(f[k] - b);
+  }
+  a.s = t[0] + t[1];
+  a.template join_group<NT>(sm);
+  if (threadIdx.x == 0) {
+    const double l = a.lse();
+    const float lp = static_cast<float>(picked - l);
+    const int64_t seq = static_cast<uint32_t>(r) / static_cast<uint32_t>(positions);
+    lse[r] = told[0] = static_cast<float>(l);
+    logp[r] = lp;
+    terms[r] = policy_row(how, inputs, weight.at(seq), r, seq, lp, slope);
+    told[1] = scale * slope[r];
+  }
+  __syncthreads();
+  const RowGrad grad(told[1], told[0], static_cast<int>(label));
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    float f[V];
+    widened(i, f);
+    if (j + i * NT * V < p.last) store_vec<Io>(o + j + i * NT * V, grad.piece<Io>(raw[i], j + i * NT * V));
+  }
+  if (column >= 0) {
+    const float q = grad.at(extra);
+    o[column] = Io::narrow(column == grad.label ? grad.g + q : q);
   }
 }
 
