@@ -42,8 +42,6 @@ from .finetune import (  # noqa: F401
     PreferenceLoss,
     clip_grad_norm,
     clip_grad_norm_,
-    finetune_lib,
-    finetune_lib_path,
     grad_norm,
     layer_norm,
     layer_norm_bwd,

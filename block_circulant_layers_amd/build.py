@@ -4,7 +4,8 @@
 
 Steps: generate csrc/twiddles.inc from float64 math, then one hipcc call each
 for librdfft.so, libfinetune.so (csrc/finetune: the operators of a fine-tuning
-step around the layers) and libstreamprobe.so (the in-place streaming pass
+step around the layers, with one g++ call for the Python module on it) and
+libstreamprobe.so (the in-place streaming pass
 that bench.py measures the transforms against).  Packed FP32 instructions are
 disabled for all device code.
 
@@ -27,8 +28,11 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "librdfft.so")
 # the operators of a fine-tuning step around the layers (include/finetune.h)
 FINETUNE_LIB = os.path.join(LIBDIR, "libfinetune.so")
+# the Python module that calls it on torch tensors
+FINETUNE_HOST = os.path.join(LIBDIR, "_finetune_host.so")
 # the in-place streaming pass bench.py measures the transforms against
 PROBE_LIB = os.path.join(LIBDIR, "libstreamprobe.so")
+CXX = os.environ.get("CXX", "g++")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 LLVM_BIN = os.environ.get("RDFFT_LLVM_BIN", "/opt/rocm/llvm/bin")
 OFFLOAD_TARGET = "hipv4-amdgcn-amd-amdhsa--gfx950"
@@ -67,15 +71,33 @@ def build(verbose: bool = True) -> str:
     return LIB
 
 
-def build_finetune(verbose: bool = True) -> str:
+def build_finetune(verbose: bool = True, host: bool = True) -> str:
+    """libfinetune.so and (``host``) the Python module on it."""
     os.makedirs(LIBDIR, exist_ok=True)
+    src = os.path.join(CSRC, "finetune")
     tmp = FINETUNE_LIB + ".tmp"
-    cmd = [HIPCC, *HIP_FLAGS, "-I", os.path.join(ROOT, "include"),
-           os.path.join(CSRC, "finetune", "finetune_lib.hip"), "-o", tmp]
+    cmd = [HIPCC, *HIP_FLAGS, "-Wl,-soname,libfinetune.so", "-I", os.path.join(ROOT, "include"),
+           os.path.join(src, "finetune_lib.hip"), "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, FINETUNE_LIB)
+    if host:
+        import sysconfig
+
+        from torch.utils import cpp_extension
+
+        includes = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include"), *cpp_extension.include_paths("cuda")]
+        tmp = FINETUNE_HOST + ".tmp"
+        cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+               "-D__HIP_PLATFORM_AMD__=1",
+               "-DTORCH_EXTENSION_NAME=_finetune_host", *[f for i in includes for f in ("-isystem", i)],
+               os.path.join(src, "finetune_host.cpp"), "-o", tmp, "-L", LIBDIR, "-lfinetune", "-Wl,-rpath,$ORIGIN",
+               *[f for i in cpp_extension.library_paths() for f in ("-L", i)], "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, FINETUNE_HOST)
     return FINETUNE_LIB
 
 
