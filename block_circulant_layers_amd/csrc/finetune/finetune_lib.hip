@@ -360,24 +360,17 @@ int launch_policy_step(const finetune_logits* in, const PolicyCall& c, float sca
 
 // ---- gradient tensors -----------------------------------------------------
 
-int64_t clip_chunks(const finetune_tensor* t, int64_t n) {
-  int64_t c = 0;
-  for (int64_t i = 0; i < n; ++i) c += ceil_div(t[i].count, kClipChunk);
-  return c;
-}
-
-// f(table, first chunk of the launch, chunks) for tables of up to kClipTensors tensors
+// f(table, chunks) for tables of up to kClipTensors tensors, the chunks of a
+// launch below 2^24
 template <class F>
 int for_tables(const finetune_tensor* t, int64_t n, F f) {
+  constexpr int64_t kMost = int64_t(1) << 23;
   ClipTable table;
   table.n = 0;
   table.first[0] = 0;
-  int64_t base = 0;
   auto flush = [&]() {
     if (table.n == 0) return static_cast<int>(RDFFT_OK);
-    const int chunks = table.first[table.n];
-    const int st = f(table, base, chunks);
-    base += chunks;
+    const int st = f(table, table.first[table.n]);
     table.n = 0;
     return st;
   };
@@ -387,18 +380,17 @@ int for_tables(const finetune_tensor* t, int64_t n, F f) {
     const char* g = static_cast<const char*>(t[i].grad);
     char* o = static_cast<char*>(t[i].out);
     while (left > 0) {
-      // chunk numbers of a launch stay below 2^24
-      const int64_t take = std::min<int64_t>(left, int64_t(kClipChunk) << 20);
+      const int64_t take = std::min<int64_t>(left, kMost * kClipChunk), chunks = ceil_div(take, kClipChunk);
       const int k = table.n++;
       table.in[k] = g;
       table.out[k] = o;
-      table.count[k] = take;
-      table.dtype[k] = static_cast<int8_t>(t[i].dtype);
-      table.first[k + 1] = table.first[k] + static_cast<int>(ceil_div(take, kClipChunk));
+      table.last[k] = static_cast<int>(take - (chunks - 1) * kClipChunk) |
+                      static_cast<int>(t[i].dtype) << kClipTypeShift;
+      table.first[k + 1] = table.first[k] + static_cast<int>(chunks);
       left -= take;
       g += take * e;
       if (o) o += take * e;
-      if (table.n == kClipTensors || table.first[table.n] >= (1 << 23)) {
+      if (table.n == kClipTensors || table.first[table.n] >= kMost) {
         const int st = flush();
         if (st != RDFFT_OK) return st;
       }
@@ -407,20 +399,42 @@ int for_tables(const finetune_tensor* t, int64_t n, F f) {
   return flush();
 }
 
-int64_t clip_workspace(const finetune_tensor* t, int64_t n) { return 16 + (clip_chunks(t, n) * 8 + 15) / 16 * 16; }
+unsigned clip_grid(int chunks) { return static_cast<unsigned>(std::min(chunks, kClipGroups)); }
 
-int launch_norm(const finetune_tensor* t, int64_t n, double max_norm, double eps, float* norm, void* ws,
-                bool with_factor, hipStream_t s) {
-  auto* partial = reinterpret_cast<double*>(static_cast<char*>(ws) + 16);
-  int st = for_tables(t, n, [&](const ClipTable& table, int64_t base, int chunks) {
-    hipLaunchKernelGGL((grad_square_kernel), dim3(static_cast<unsigned>(chunks)), dim3(kClipThreads), 0, s, table,
-                       partial + base);
+// partial sums of all launches
+int64_t clip_parts(const finetune_tensor* t, int64_t n) {
+  int64_t parts = 0;
+  for_tables(t, n, [&](const ClipTable&, int chunks) {
+    parts += clip_grid(chunks);
+    return static_cast<int>(RDFFT_OK);
+  });
+  return parts;
+}
+
+int64_t clip_workspace(const finetune_tensor* t, int64_t n) { return (clip_parts(t, n) * 8 + 15) / 16 * 16; }
+
+int launch_squares(const finetune_tensor* t, int64_t n, double* partial, hipStream_t s) {
+  return for_tables(t, n, [&](const ClipTable& table, int chunks) {
+    hipLaunchKernelGGL((grad_square_kernel), dim3(clip_grid(chunks)), dim3(kClipThreads), 0, s, table, partial);
+    partial += clip_grid(chunks);
     return launch_status();
   });
-  if (st != RDFFT_OK) return st;
-  hipLaunchKernelGGL((grad_norm_kernel), dim3(1), dim3(kClipThreads), 0, s, partial, clip_chunks(t, n), max_norm, eps,
-                     norm, with_factor ? static_cast<float*>(ws) : nullptr);
+}
+
+int launch_norm(const double* partial, int64_t parts, float* norm, hipStream_t s) {
+  hipLaunchKernelGGL((grad_norm_kernel), dim3(1), dim3(kClipThreads), 0, s, partial, parts, norm);
   return launch_status();
+}
+
+// the launches over the tables, the first of them with the norm's address
+int launch_scale(const finetune_tensor* t, int64_t n, const double* partial, int64_t parts, double max_norm,
+                 double eps, float* norm, hipStream_t s) {
+  return for_tables(t, n, [&](const ClipTable& table, int chunks) {
+    hipLaunchKernelGGL((grad_scale_kernel), dim3(clip_grid(chunks)), dim3(kClipThreads), 0, s, table, partial, parts,
+                       max_norm, eps, norm);
+    norm = nullptr;
+    return launch_status();
+  });
 }
 
 }  // namespace
@@ -625,30 +639,28 @@ int grad_norm_workspace(const finetune_tensor* tensors, int64_t n, int64_t* byte
 
 int grad_norm(const finetune_tensor* tensors, int64_t n, float* norm, void* ws, int64_t ws_bytes, void* stream) {
   int st = check_tensors(tensors, n, false);
-  if (st == RDFFT_OK && norm == nullptr) st = RDFFT_ERR_NULL;
-  if (st == RDFFT_OK && !aligned_to(norm, 4)) st = RDFFT_ERR_ALIGN;
-  if (st == RDFFT_OK) st = check_workspace(ws, ws_bytes, clip_workspace(tensors, n));
+  if (st == RDFFT_OK) st = check_norm_buffers(tensors, n, false, norm, ws, ws_bytes, clip_workspace(tensors, n));
   if (st != RDFFT_OK) return st;
-  return launch_norm(tensors, n, 0.0, 0.0, norm, ws, false, static_cast<hipStream_t>(stream));
+  auto* partial = static_cast<double*>(ws);
+  st = launch_squares(tensors, n, partial, static_cast<hipStream_t>(stream));
+  if (st != RDFFT_OK) return st;
+  return launch_norm(partial, clip_parts(tensors, n), norm, static_cast<hipStream_t>(stream));
 }
 
 int clip_grad_norm(const finetune_tensor* tensors, int64_t n, double max_norm, double eps, float* norm, void* ws,
                    int64_t ws_bytes, void* stream) {
   int st = check_tensors(tensors, n, true);
   if (st == RDFFT_OK && (!(max_norm >= 0.0) || !(eps >= 0.0))) st = RDFFT_ERR_SIZE;
-  if (st == RDFFT_OK && norm == nullptr) st = RDFFT_ERR_NULL;
-  if (st == RDFFT_OK && !aligned_to(norm, 4)) st = RDFFT_ERR_ALIGN;
-  if (st == RDFFT_OK) st = check_workspace(ws, ws_bytes, clip_workspace(tensors, n));
+  if (st == RDFFT_OK) st = check_norm_buffers(tensors, n, true, norm, ws, ws_bytes, clip_workspace(tensors, n));
   if (st == RDFFT_OK) st = check_tensor_aliases(tensors, n);
   if (st != RDFFT_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  st = launch_norm(tensors, n, max_norm, eps, norm, ws, true, s);
+  auto* partial = static_cast<double*>(ws);
+  const int64_t parts = clip_parts(tensors, n);
+  st = launch_squares(tensors, n, partial, s);
   if (st != RDFFT_OK) return st;
-  return for_tables(tensors, n, [&](const ClipTable& table, int64_t, int chunks) {
-    hipLaunchKernelGGL((grad_scale_kernel), dim3(static_cast<unsigned>(chunks)), dim3(kClipThreads), 0, s, table,
-                       static_cast<const float*>(ws));
-    return launch_status();
-  });
+  if (parts == 0) return launch_norm(partial, 0, norm, s);  // no elements at all
+  return launch_scale(tensors, n, partial, parts, max_norm, eps, norm, s);
 }
 
 }  // extern "C"

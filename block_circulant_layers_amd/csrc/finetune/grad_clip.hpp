@@ -12,18 +12,20 @@
 namespace finetune {
 
 constexpr int kClipThreads = 256;
-constexpr int kClipChunk = 16384;  // elements of one workgroup
-constexpr int kClipTensors = 112;  // tensors of one launch (the table travels in the kernel's arguments)
+constexpr int kClipChunk = 8192;    // elements of one unit of work
+constexpr int kClipTensors = 144;   // tensors of one launch (the table travels in the kernel's arguments)
+constexpr int kClipGroups = 2048;   // workgroups of a launch at most: 8 a compute unit, and one partial sum each
 
 struct ClipTable {
   const void* in[kClipTensors];
   void* out[kClipTensors];
-  int64_t count[kClipTensors];
-  int first[kClipTensors + 1];  // first chunk of each tensor within the launch
-  int8_t dtype[kClipTensors];
+  int last[kClipTensors];           // elements of each tensor's last chunk; 2 bits of type above them
+  int first[kClipTensors + 1];      // first chunk of each tensor within the launch
   int n;
 };
-static_assert(sizeof(ClipTable) <= 3800, "kernel arguments are limited to 4 KB");
+static_assert(sizeof(ClipTable) <= 3600, "kernel arguments are limited to 4 KB");
+constexpr int kClipTypeShift = 16;
+static_assert(kClipChunk < 1 << kClipTypeShift);
 
 // The tensor that chunk c belongs to: the last whose first chunk is <= c.
 __device__ __forceinline__ int tensor_of(const ClipTable& t, int c) {
@@ -38,67 +40,105 @@ __device__ __forceinline__ int tensor_of(const ClipTable& t, int c) {
   return lo;
 }
 
-template <class Io>
-__device__ __forceinline__ double chunk_square(const void* p, int64_t begin, int64_t end) {
-  const auto* g = static_cast<const typename Io::T*>(p);
-  double a = 0.0;
-  for (int64_t i = begin + threadIdx.x; i < end; i += kClipThreads) {
-    const double v = Io::widen(g[i]);
-    a += v * v;
-  }
-  return a;
+// f(storage type, pointer in, pointer out, elements) for chunk c
+template <class F>
+__device__ __forceinline__ void for_chunk(const ClipTable& t, int c, F f) {
+  const int i = tensor_of(t, c), type = t.last[i] >> kClipTypeShift;
+  const int64_t begin = static_cast<int64_t>(c - t.first[i]) * kClipChunk;
+  const int n = c + 1 == t.first[i + 1] ? t.last[i] & ((1 << kClipTypeShift) - 1) : kClipChunk;
+  const auto with = [&](auto io) {
+    using T = typename decltype(io)::T;
+    f(io, static_cast<const T*>(t.in[i]) + begin, static_cast<T*>(t.out[i]) + begin, n);
+  };
+  if (type == 0)
+    with(F32{});
+  else if (type == 1)
+    with(Bf16{});
+  else
+    with(F16{});
 }
 
-// partial[base + c] = the sum of squares of chunk c
+// partial[workgroup] = the sum of squares of the chunks it walks over
 __global__ void __launch_bounds__(kClipThreads) grad_square_kernel(ClipTable t, double* partial) {
   __shared__ double s[kClipThreads / kWave];
-  const int c = blockIdx.x, i = tensor_of(t, c);
-  const int64_t begin = static_cast<int64_t>(c - t.first[i]) * kClipChunk;
-  const int64_t end = begin + kClipChunk < t.count[i] ? begin + kClipChunk : t.count[i];
-  double a;
-  if (t.dtype[i] == 0)
-    a = chunk_square<F32>(t.in[i], begin, end);
-  else if (t.dtype[i] == 1)
-    a = chunk_square<Bf16>(t.in[i], begin, end);
-  else
-    a = chunk_square<F16>(t.in[i], begin, end);
-  a = block_sum<kClipThreads>(a, s);
-  if (threadIdx.x == 0) partial[c] = a;
+  double a[2] = {0.0, 0.0};
+  const int chunks = t.first[t.n];
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x)
+    for_chunk(t, c, [&](auto io, const auto* g, auto*, int n) {
+      using Io = decltype(io);
+      constexpr int V = Io::kVec, U = 4;
+      const auto add = [&](auto v, int k) {
+        const double x = Io::widen(v);
+        a[k % 2] = __builtin_fma(x, x, a[k % 2]);
+      };
+      const Pieces<Io> p(g, 0, n);
+      int j = p.first + static_cast<int>(threadIdx.x) * V;
+      for (; j + (U - 1) * kClipThreads * V < p.last; j += U * kClipThreads * V) {
+        typename Io::Vec raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = load_vec<Io>(g + j + u * kClipThreads * V);
+#pragma unroll
+        for (int k = 0; k < U * V; ++k) add(raw[k / V][k % V], k);
+      }
+      for (; j < p.last; j += kClipThreads * V) {
+        const typename Io::Vec raw = load_vec<Io>(g + j);
+#pragma unroll
+        for (int k = 0; k < V; ++k) add(raw[k], k);
+      }
+      p.template rest<kClipThreads>([&](int i) { add(g[i], 0); });
+    });
+  const double all = block_sum<kClipThreads>(a[0] + a[1], s);
+  if (threadIdx.x == 0) partial[blockIdx.x] = all;
 }
 
-// norm and the factor (factor[0]) from n partial sums, in order
-__global__ void __launch_bounds__(kClipThreads)
-    grad_norm_kernel(const double* partial, int64_t n, double max_norm, double eps, float* norm, float* factor) {
-  __shared__ double s[kClipThreads / kWave];
+// The norm from n partial sums, in a fixed order, in every thread of the workgroup.
+__device__ __forceinline__ double norm_of(const double* partial, int64_t n, double* s) {
   double a = 0.0;
+#pragma unroll 8
   for (int64_t i = threadIdx.x; i < n; i += kClipThreads) a += partial[i];
-  a = sqrt(block_sum<kClipThreads>(a, s));
-  if (threadIdx.x == 0) {
-    norm[0] = static_cast<float>(a);
-    const double f = max_norm / (a + eps);
-    if (factor) factor[0] = f > 1.0 ? 1.0f : static_cast<float>(f);
-  }
+  return sqrt(block_sum<kClipThreads>(a, s));
 }
 
-template <class Io>
-__device__ __forceinline__ void chunk_scale(const void* p, void* q, int64_t begin, int64_t end, float f) {
-  const auto* g = static_cast<const typename Io::T*>(p);
-  auto* o = static_cast<typename Io::T*>(q);
-  for (int64_t i = begin + threadIdx.x; i < end; i += kClipThreads) o[i] = Io::narrow(Io::widen(g[i]) * f);
+__global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const double* partial, int64_t n, float* norm) {
+  __shared__ double s[kClipThreads / kWave];
+  const double a = norm_of(partial, n, s);
+  if (threadIdx.x == 0) norm[0] = static_cast<float>(a);
 }
 
-__global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(ClipTable t, const float* factor) {
-  const int c = blockIdx.x, i = tensor_of(t, c);
-  const float f = factor[0];
-  if (f == 1.0f && t.in[i] == t.out[i]) return;  // nothing to change in place
-  const int64_t begin = static_cast<int64_t>(c - t.first[i]) * kClipChunk;
-  const int64_t end = begin + kClipChunk < t.count[i] ? begin + kClipChunk : t.count[i];
-  if (t.dtype[i] == 0)
-    chunk_scale<F32>(t.in[i], t.out[i], begin, end, f);
-  else if (t.dtype[i] == 1)
-    chunk_scale<Bf16>(t.in[i], t.out[i], begin, end, f);
-  else
-    chunk_scale<F16>(t.in[i], t.out[i], begin, end, f);
+// out = g min(1, max / (norm + eps)).  Every workgroup sums the partial sums
+// itself (16 KB from L2 at most a launch of squares) instead of waiting for a
+// kernel that does.  The chunks come in the reverse of the order in which their
+// squares were read, so that the last ones read are still in the 256 MB cache.
+__global__ void __launch_bounds__(kClipThreads)
+    grad_scale_kernel(ClipTable t, const double* partial, int64_t parts, double max_norm, double eps, float* norm) {
+  __shared__ double s[kClipThreads / kWave];
+  const double a = norm_of(partial, parts, s);
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = static_cast<float>(a);
+  const double q = max_norm / (a + eps);
+  const float f = q > 1.0 ? 1.0f : static_cast<float>(q);
+  const int chunks = t.first[t.n];
+  for (int c = chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x)
+    for_chunk(t, c, [&](auto io, const auto* g, auto* o, int n) {
+      using Io = decltype(io);
+      constexpr int V = Io::kVec, U = 4;
+      if (f == 1.0f && g == o) return;  // nothing to change in place
+      const Pieces<Io> p(o, 0, n);
+      int j = p.first + static_cast<int>(threadIdx.x) * V;
+      const auto scaled = [&](typename Io::Vec v) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = Io::narrow(Io::widen(v[k]) * f);
+        return v;
+      };
+      for (; j + (U - 1) * kClipThreads * V < p.last; j += U * kClipThreads * V) {
+        typename Io::Vec raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = load_vec<Io>(g + j + u * kClipThreads * V);
+#pragma unroll
+        for (int u = 0; u < U; ++u) store_vec<Io>(o + j + u * kClipThreads * V, scaled(raw[u]));
+      }
+      for (; j < p.last; j += kClipThreads * V) store_vec<Io>(o + j, scaled(load_vec<Io>(g + j)));
+      p.template rest<kClipThreads>([&](int i) { o[i] = Io::narrow(Io::widen(g[i]) * f); });
+    });
 }
 
 }  // namespace finetune

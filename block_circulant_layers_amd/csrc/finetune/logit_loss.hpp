@@ -99,39 +99,6 @@ struct MaxSum {
   __device__ __forceinline__ double lse() const { return m + log(static_cast<double>(s)) + (m - m); }
 };
 
-template <class Io>
-__device__ __forceinline__ typename Io::Vec load_vec(const typename Io::T* p) {
-  return *reinterpret_cast<const typename Io::Vec*>(p);
-}
-template <class Io>
-__device__ __forceinline__ void store_vec(typename Io::T* p, typename Io::Vec v) {
-  *reinterpret_cast<typename Io::Vec*>(p) = v;
-}
-
-// The columns [begin, end) of a row (rows start at any element): 16-byte pieces
-// from the first 128-byte line on, up to `last`, and the columns before and
-// after them.  Pieces at odd addresses straddle lines: reading 5808 rows of
-// 50001 bf16 took 170 us from the row's start, 148 us from the first address
-// divisible by 16, and 141 us from the first line on (their gradient: 281, 260,
-// 248 us).
-template <class Io, int LINE = 128>
-struct Pieces {
-  int begin, first, last, end;
-  __device__ __forceinline__ Pieces(const typename Io::T* row, int b, int e) : begin(b), end(e) {
-    constexpr int S = sizeof(typename Io::T), L = LINE / S;
-    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row + b) / S % L);
-    first = b + (L - off) % L;
-    if (first > e) first = e;
-    last = first + (e - first) / Io::kVec * Io::kVec;
-  }
-  // f(column) for the columns outside the pieces
-  template <int NT, class F>
-  __device__ __forceinline__ void rest(F f) const {
-    const int head = first - begin, n = head + end - last;
-    for (int t = threadIdx.x; t < n; t += NT) f(t < head ? begin + t : last + t - head);
-  }
-};
-
 // Maximum and sum of the columns [begin, end) of a row by NT threads, four
 // 16-byte pieces of a thread in flight.
 template <class Io, int NT>

@@ -241,6 +241,23 @@ inline int check_tensors(const finetune_tensor* t, int64_t n, bool with_out) {
   return RDFFT_OK;
 }
 
+// the norm and the workspace lie apart from each other and from every tensor
+inline int check_norm_buffers(const finetune_tensor* t, int64_t n, bool with_out, const float* norm, const void* ws,
+                              int64_t ws_bytes, int64_t need) {
+  if (norm == nullptr) return RDFFT_ERR_NULL;
+  if (!aligned_to(norm, 4)) return RDFFT_ERR_ALIGN;
+  const int st = check_workspace(ws, ws_bytes, need);
+  if (st != RDFFT_OK) return st;
+  const Range rn{norm, 4}, rw{ws, need};
+  if (clashes(rn, rw)) return RDFFT_ERR_ALIAS;
+  for (int64_t i = 0; i < n; ++i) {
+    const int64_t bytes = t[i].count * dtype_bytes(int(t[i].dtype));
+    const Range g{t[i].grad, bytes}, o{with_out ? t[i].out : nullptr, bytes};
+    if (clashes(rn, g) || clashes(rn, o) || clashes(rw, g) || clashes(rw, o)) return RDFFT_ERR_ALIAS;
+  }
+  return RDFFT_OK;
+}
+
 // No element is written twice, and none is written that another tensor reads.
 // Buffers that come in address order (a bucket's tensors, as they mostly do)
 // are seen to be apart in one pass; any other order is sorted first.
