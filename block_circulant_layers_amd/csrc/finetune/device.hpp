@@ -124,13 +124,22 @@ __device__ __forceinline__ V block_sum(V v, V* s) {
   return group_sum<NT>(v, s);
 }
 
-template <class Io>
+// 16 bytes of elements.  STREAM: past the caches, for what is too large to be
+// found there again (1 GiB read at 7.0 TB/s against 6.2, copied at 6.0 against
+// 5.4 with the same loop).
+template <class Io, bool STREAM = false>
 __device__ __forceinline__ typename Io::Vec load_vec(const typename Io::T* p) {
-  return *reinterpret_cast<const typename Io::Vec*>(p);
+  const auto* v = reinterpret_cast<const typename Io::Vec*>(p);
+  if constexpr (STREAM) return __builtin_nontemporal_load(v);
+  return *v;
 }
-template <class Io>
+template <class Io, bool STREAM = false>
 __device__ __forceinline__ void store_vec(typename Io::T* p, typename Io::Vec v) {
-  *reinterpret_cast<typename Io::Vec*>(p) = v;
+  auto* q = reinterpret_cast<typename Io::Vec*>(p);
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(v, q);
+  else
+    *q = v;
 }
 
 // The columns [begin, end) of a row (rows start at any element): 16-byte pieces

@@ -25,6 +25,17 @@ int by_dtype(int64_t dtype, F f) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Buffers of a call from which on its loads and stores go past the caches: half
+// of the 256 MB cache, so that what the next call reads again stays in it.
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
+template <class F>
+void by_stream(bool stream, F f) {
+  if (stream)
+    f(std::true_type{});
+  else
+    f(std::false_type{});
+}
+
 constexpr int64_t kMaxGrid = 1 << 20;
 unsigned grid_of(int64_t n) { return static_cast<unsigned>(n < kMaxGrid ? n : kMaxGrid); }
 
@@ -192,16 +203,24 @@ JoinParts<Io> join_of(const finetune_logits* in, const RowSplit& split, float* l
           static_cast<int>(in->vocab)};
 }
 
+// whether the logits are too large to be found in the caches again
+bool streams(const finetune_logits* in) {
+  return logit_rows(in) * in->vocab * dtype_bytes(static_cast<int>(in->dtype)) > kStreamBytes;
+}
+
 // the rows' log-probabilities, or, where rows are split, their parts
 template <class Io>
 int launch_rows(const finetune_logits* in, const RowSplit& split, float* logp, float* lse, void* ws, hipStream_t s) {
   const int64_t rows = logit_rows(in);
   if (rows == 0) return RDFFT_OK;
   by_threads(split.nt, [&](auto nt) {
-    constexpr int NT = decltype(nt)::value;
-    hipLaunchKernelGGL((token_logprob_kernel<Io, NT>), dim3(grid_of(rows * split.parts)), dim3(NT), 0, s,
-                       rows_of<Io>(in), in->labels, logp, lse, at<float2>(ws, LogitsWorkspace(in).parts), rows, in->positions,
-                       static_cast<int>(in->vocab), split.parts, split.per);
+    by_stream(streams(in), [&](auto stream) {
+      constexpr int NT = decltype(nt)::value;
+      hipLaunchKernelGGL((token_logprob_kernel<Io, NT, decltype(stream)::value>), dim3(grid_of(rows * split.parts)),
+                         dim3(NT), 0, s, rows_of<Io>(in), in->labels, logp, lse,
+                         at<float2>(ws, LogitsWorkspace(in).parts), rows, in->positions,
+                         static_cast<int>(in->vocab), split.parts, split.per);
+    });
   });
   return launch_status();
 }
@@ -228,10 +247,12 @@ int launch_grad(const finetune_logits* in, const float* lse, const RowScale& sca
     using Io = decltype(io);
     const RowSplit split = row_split(in);
     by_threads(split.nt, [&](auto nt) {
-      constexpr int NT = decltype(nt)::value;
-      hipLaunchKernelGGL((logits_grad_kernel<Io, NT>), dim3(grid_of(rows * split.parts)), dim3(NT), 0, s,
-                         rows_of<Io>(in), in->labels, lse, scale, rows_of<Io>(out), rows, in->positions,
-                         static_cast<int>(in->vocab), split.parts, split.per);
+      by_stream(streams(in), [&](auto stream) {
+        constexpr int NT = decltype(nt)::value;
+        hipLaunchKernelGGL((logits_grad_kernel<Io, NT, decltype(stream)::value>), dim3(grid_of(rows * split.parts)),
+                           dim3(NT), 0, s, rows_of<Io>(in), in->labels, lse, scale, rows_of<Io>(out), rows,
+                           in->positions, static_cast<int>(in->vocab), split.parts, split.per);
+      });
     });
     return launch_status();
   });
@@ -348,10 +369,13 @@ int launch_policy_step(const finetune_logits* in, const PolicyCall& c, float sca
   st = by_dtype(in->dtype, [&](auto io) {
     using Io = decltype(io);
     by_held_row(in, [&](auto nt, auto r) {
-      constexpr int NT = decltype(nt)::value, R = decltype(r)::value;
-      hipLaunchKernelGGL((policy_step_kernel<Io, NT, R>), dim3(static_cast<unsigned>(logit_rows(in))), dim3(NT), 0, s,
-                         rows_of<Io>(in), in->labels, c.in, c.weight, c.how, scale, logp, lse, slope, c.terms,
-                         rows_of<Io>(out), in->positions, static_cast<int>(in->vocab));
+      by_stream(streams(in), [&](auto stream) {
+        constexpr int NT = decltype(nt)::value, R = decltype(r)::value;
+        hipLaunchKernelGGL((policy_step_kernel<Io, NT, R, decltype(stream)::value>),
+                           dim3(static_cast<unsigned>(logit_rows(in))), dim3(NT), 0, s, rows_of<Io>(in), in->labels,
+                           c.in, c.weight, c.how, scale, logp, lse, slope, c.terms, rows_of<Io>(out), in->positions,
+                           static_cast<int>(in->vocab));
+      });
     });
     return launch_status();
   });

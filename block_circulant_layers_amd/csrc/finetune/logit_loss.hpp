@@ -101,7 +101,7 @@ struct MaxSum {
 
 // Maximum and sum of the columns [begin, end) of a row by NT threads, four
 // 16-byte pieces of a thread in flight.
-template <class Io, int NT>
+template <class Io, int NT, bool STREAM>
 __device__ __forceinline__ MaxSum row_max_sum(const typename Io::T* x, int begin, int end) {
   constexpr int V = Io::kVec, U = 4;
   const Pieces<Io> p(x, begin, end);
@@ -110,14 +110,14 @@ __device__ __forceinline__ MaxSum row_max_sum(const typename Io::T* x, int begin
   for (; j + (U - 1) * NT * V + V <= p.last; j += U * NT * V) {
     typename Io::Vec raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = load_vec<Io>(x + j + u * NT * V);
+    for (int u = 0; u < U; ++u) raw[u] = load_vec<Io, STREAM>(x + j + u * NT * V);
     float f[U * V];
 #pragma unroll
     for (int k = 0; k < U * V; ++k) f[k] = Io::widen(raw[k / V][k % V]);
     a.add(f);
   }
   for (; j < p.last; j += NT * V) {
-    const typename Io::Vec raw = load_vec<Io>(x + j);
+    const typename Io::Vec raw = load_vec<Io, STREAM>(x + j);
     float f[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) f[k] = Io::widen(raw[k]);
@@ -134,7 +134,7 @@ __device__ __forceinline__ MaxSum row_max_sum(const typename Io::T* x, int begin
 // there are fewer rows than the chip has room for, `parts` workgroups of `per`
 // columns each, whose maxima and sums go to `partial` for the next kernel to
 // join.
-template <class Io, int NT>
+template <class Io, int NT, bool STREAM>
 __global__ void __launch_bounds__(NT)
     token_logprob_kernel(Rows<Io> in, const int64_t* labels, float* logp, float* lse, float2* partial, int64_t rows,
                          int64_t positions, int v, int parts, int per) {
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(NT)
     }
     const typename Io::T* x = in.row(r, positions);
     const int begin = static_cast<int>(i - r * parts) * per, end = begin + per < v ? begin + per : v;
-    MaxSum a = row_max_sum<Io, NT>(x, begin, end);
+    MaxSum a = row_max_sum<Io, NT, STREAM>(x, begin, end);
     a.template join_group<NT>(sm);
     if (threadIdx.x == 0) {
       if (parts > 1) {
@@ -241,7 +241,7 @@ struct RowScale {
 };
 
 // The gradient of every row, `parts` workgroups of `per` columns a row.
-template <class Io, int NT>
+template <class Io, int NT, bool STREAM>
 __global__ void __launch_bounds__(NT)
     logits_grad_kernel(Rows<Io> in, const int64_t* labels, const float* lse, RowScale scale, Rows<Io> out,
                        int64_t rows, int64_t positions, int v, int parts, int per) {
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(NT)
     if (label == kIgnore) {
       const Pieces<Io> p(o, begin, end);
       for (int j = p.first + static_cast<int>(threadIdx.x) * V; j < p.last; j += NT * V)
-        store_vec<Io>(o + j, typename Io::Vec{});
+        store_vec<Io, STREAM>(o + j, typename Io::Vec{});
       p.template rest<NT>([&](int c) { o[c] = 0; });
       continue;
     }
@@ -266,11 +266,11 @@ __global__ void __launch_bounds__(NT)
     for (; j + (U - 1) * NT * V + V <= p.last; j += U * NT * V) {
       typename Io::Vec raw[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = load_vec<Io>(x + j + u * NT * V);
+      for (int u = 0; u < U; ++u) raw[u] = load_vec<Io, STREAM>(x + j + u * NT * V);
 #pragma unroll
-      for (int u = 0; u < U; ++u) store_vec<Io>(o + j + u * NT * V, grad.piece<Io>(raw[u], j + u * NT * V));
+      for (int u = 0; u < U; ++u) store_vec<Io, STREAM>(o + j + u * NT * V, grad.piece<Io>(raw[u], j + u * NT * V));
     }
-    for (; j < p.last; j += NT * V) store_vec<Io>(o + j, grad.piece<Io>(load_vec<Io>(x + j), j));
+    for (; j < p.last; j += NT * V) store_vec<Io, STREAM>(o + j, grad.piece<Io>(load_vec<Io, STREAM>(x + j), j));
     p.template rest<NT>([&](int c) {
       const float q = grad.at(Io::widen(x[c]));
       o[c] = Io::narrow(c == grad.label ? grad.g + q : q);
@@ -495,7 +495,7 @@ __device__ __forceinline__ typename Io::Vec lowest_vec() {
   return v;
 }
 
-template <class Io, int NT, int R>
+template <class Io, int NT, int R, bool STREAM>
 __global__ void __launch_bounds__(NT, 4)  // 128 registers: 16 waves a compute unit
     policy_step_kernel(Rows<Io> in, const int64_t* labels, PolicyInputs inputs, PolicyWeight weight, Policy how,
                        float scale, float* logp, float* lse, float* slope, double2* terms, Rows<Io> out,
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(NT, 4)  // 128 registers: 16 waves a compute u
 #pragma unroll
     for (int k = 0; k < V; ++k) f[k] = Io::narrow(fill);
     const Pieces<Io> p(o, 0, v);
-    for (int j = p.first + static_cast<int>(threadIdx.x) * V; j < p.last; j += NT * V) store_vec<Io>(o + j, f);
+    for (int j = p.first + static_cast<int>(threadIdx.x) * V; j < p.last; j += NT * V) store_vec<Io, STREAM>(o + j, f);
     p.template rest<NT>([&](int c) { o[c] = f[0]; });
     if (threadIdx.x == 0) {
       logp[r] = lse[r] = slope[r] = fill;
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(NT, 4)  // 128 registers: 16 waves a compute u
   typename Io::Vec raw[R];
   int j = p.first + static_cast<int>(threadIdx.x) * V;
 #pragma unroll
-  for (int i = 0; i < R; ++i) raw[i] = j + i * NT * V < p.last ? load_vec<Io>(x + j + i * NT * V) : lowest_vec<Io>();
+  for (int i = 0; i < R; ++i) raw[i] = j + i * NT * V < p.last ? load_vec<Io, STREAM>(x + j + i * NT * V) : lowest_vec<Io>();
   int column = -1;
   p.template rest<NT>([&](int c) { column = c; });
   const float extra = column >= 0 ? Io::widen(x[column]) : -INFINITY;
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(NT, 4)  // 128 registers: 16 waves a compute u
   for (int i = 0; i < R; ++i) {
     float f[V];
     widened(i, f);
-    if (j + i * NT * V < p.last) store_vec<Io>(o + j + i * NT * V, grad.piece<Io>(raw[i], j + i * NT * V));
+    if (j + i * NT * V < p.last) store_vec<Io, STREAM>(o + j + i * NT * V, grad.piece<Io>(raw[i], j + i * NT * V));
   }
   if (column >= 0) {
     const float q = grad.at(extra);
