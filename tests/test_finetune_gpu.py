@@ -679,3 +679,44 @@ def test_another_stream():
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,v", [("f32", 5003), ("bf16", 4099), ("f16", 16390), ("bf16", 50001), ("f32", 33001),
+                                     ("bf16", 131072), ("f16", 140001)])
+def test_policy_step_many_rows(v, dtype):
+    # enough rows that a step holds them in registers: a wave a row, and workgroups of 256 to 1024 threads, and a
+    # row past the widest; few unmasked rows keep the oracle quick
+    n, t = 8, 130
+    r0 = rng(60, v)
+    lab = np.full((n, t), IGNORE)
+    live = r0.choice(n * t, size=24, replace=False)
+    lab.reshape(-1)[live] = r0.integers(0, v, size=24)
+    lab = lab.astype(np.int64)
+    g = torch.Generator(device=DEV).manual_seed(v)
+    xd = torch.randn(n, t, v, generator=g, device=DEV).mul_(3.0).to(fu.TORCH[dtype])
+    rows = f64(xd.reshape(n * t, v)[torch.from_numpy(live).to(DEV)])  # the unmasked rows alone, one sequence each
+    small = lab.reshape(-1)[live][:, None]
+    logp0, lse0 = fo.token_logprob(rows[:, None], small)
+    old, oldr = exact32(logp0 + 0.2 * r0.standard_normal(logp0.shape))
+    adv, advr = exact32(r0.standard_normal(logp0.shape))
+    _, _, slope0 = fo.policy(logp0, small, oldr, advr, reduction="token")
+    full_old = torch.zeros(n * t, device=DEV)
+    full_adv = torch.zeros(n * t, device=DEV)
+    at = torch.from_numpy(live).to(DEV)
+    full_old[at], full_adv[at] = old[:, 0], adv[:, 0]
+    r, d = bcl.policy_loss_step(xd, dev(lab, torch.int64), full_old.view(n, t), full_adv.view(n, t))
+    e = fu.lse_err(rows[:, None], lse0) + 2 * U * np.abs(logp0)
+    within(f64(r.logp.reshape(-1)[at])[:, None], logp0, e)
+    e_slope = np.abs(slope0) * (e + 4 * U) * 1.2 + 4 * U * np.abs(slope0)
+    within(f64(r.slope.reshape(-1)[at])[:, None], slope0, e_slope)
+    want = fo.logits_grad(rows[:, None], small, slope0)
+    got = f64(d.reshape(n * t, v)[at])[:, None]
+    within(got, want, fu.grad_err(want, rows[:, None], small, slope0, lse0, dtype) + e_slope[..., None])
+    d.reshape(n * t, v)[at] = 0
+    assert not d.any()
+    f = bcl.policy_loss_fwd(xd, dev(lab, torch.int64), full_old.view(n, t), full_adv.view(n, t))
+    within(f64(f.loss), f64(r.loss), 1e-6)
+    # in place
+    first = bcl.policy_loss_step(xd, dev(lab, torch.int64), full_old.view(n, t), full_adv.view(n, t))[1]
+    bcl.policy_loss_step(xd, dev(lab, torch.int64), full_old.view(n, t), full_adv.view(n, t), dlogits=xd)
+    assert torch.equal(xd, first)
