@@ -25,9 +25,12 @@ int by_dtype(int64_t dtype, F f) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Buffers of a call from which on its loads and stores go past the caches: half
-// of the 256 MB cache, so that what the next call reads again stays in it.
-constexpr int64_t kStreamBytes = int64_t(128) << 20;
+// Whether a call's large buffers of `bytes` in all go past the caches: where the
+// 256 MB cache cannot hold them until they are used again.  Both sides, layer
+// norm of rows of 4096 bf16: forward of 16384 rows (268 MB) 51 us past the
+// caches, 47 through them, of 32768 rows 101 and 107; backward of 8192 rows
+// (201 MB) 51 and 47, of 16384 rows (403 MB) 82 and 85.
+constexpr bool past_caches(int64_t bytes) { return bytes > int64_t(320) << 20; }
 template <class F>
 void by_stream(bool stream, F f) {
   if (stream)
@@ -66,9 +69,11 @@ void by_norm_row(int64_t d, F f) {
 }
 
 // Workgroups of the backward, each with one slice of the sums over rows (the
-// kernels of any length: row ranges of the column kernel).  512 workgroups of
-// 256 threads keep enough loads in flight to fill the memory system; more
-// would only make more slices to sum.
+// kernels of any length: row ranges of the column kernel).  One a compute unit
+// keeps enough loads in flight, and every other one makes slices to write and
+// sum: rows of 4096 bf16, 256 / 512 / 1024 workgroups: 2048 rows 20 / 25 / 36 us,
+// 16384 rows 80 / 86 / 102 us.  Rows of up to 1024 elements have slices small
+// enough for two a unit (32768 rows of 512: 30 / 25.5 / 27 us).
 struct DwSplit {
   int64_t parts, per;
 };
@@ -76,7 +81,7 @@ DwSplit dw_split(int64_t rows, int64_t d) {
   const int t = norm_threads(d);
   if (t) {
     const int64_t groups = ceil_div(std::max<int64_t>(rows, 1), norm_wg(t) / t);
-    return {std::min<int64_t>(groups, t == 1024 ? 256 : 512), 0};
+    return {std::min<int64_t>(groups, t >= kNormThreads ? 256 : 512), 0};
   }
   const int64_t cols = ceil_div(d, kNormThreads);
   const int64_t parts = std::max<int64_t>(std::min<int64_t>(1024 / cols, ceil_div(rows, 16)), 1);
@@ -100,8 +105,11 @@ int launch_norm_fwd(const void* x, const float* w, const float* b, void* y, floa
     constexpr int TT = decltype(t)::value, WG = norm_wg(TT);
     const int64_t groups = ceil_div(rows, WG / TT);
     const int64_t grid = std::min<int64_t>(groups, TT == 1024 ? 512 : 2048);
-    hipLaunchKernelGGL((layer_norm_fwd_kernel<Io, TT, decltype(ragged)::value>), dim3(static_cast<unsigned>(grid)),
-                       dim3(WG), 0, s, px, w, b, py, mean, rstd, rows, n, xs, ys, static_cast<float>(eps));
+    by_stream(past_caches(2 * rows * d * int64_t(sizeof(T))), [&](auto stream) {
+      hipLaunchKernelGGL((layer_norm_fwd_kernel<Io, TT, decltype(ragged)::value, decltype(stream)::value>),
+                         dim3(static_cast<unsigned>(grid)), dim3(WG), 0, s, px, w, b, py, mean, rstd, rows, n, xs, ys,
+                         static_cast<float>(eps));
+    });
   });
   return launch_status();
 }
@@ -117,9 +125,11 @@ int launch_norm_bwd(const void* x, const float* w, const float* mean, const floa
   if (norm_threads(d)) {
     by_norm_row<Io>(d, [&](auto t, auto ragged) {
       constexpr int TT = decltype(t)::value;
-      hipLaunchKernelGGL((layer_norm_bwd_kernel<Io, TT, decltype(ragged)::value>),
-                         dim3(static_cast<unsigned>(split.parts)), dim3(norm_wg(TT)), norm_bwd_lds(TT), s, px, w, mean, rstd, pg, po,
-                         ws, rows, n, xs, dys, dxs);
+      by_stream(past_caches(3 * rows * d * int64_t(sizeof(T))), [&](auto stream) {
+        hipLaunchKernelGGL((layer_norm_bwd_kernel<Io, TT, decltype(ragged)::value, decltype(stream)::value>),
+                           dim3(static_cast<unsigned>(split.parts)), dim3(norm_wg(TT)), norm_bwd_lds(TT), s, px, w,
+                           mean, rstd, pg, po, ws, rows, n, xs, dys, dxs);
+      });
     });
     return launch_status();
   }
@@ -203,9 +213,8 @@ JoinParts<Io> join_of(const finetune_logits* in, const RowSplit& split, float* l
           static_cast<int>(in->vocab)};
 }
 
-// whether the logits are too large to be found in the caches again
-bool streams(const finetune_logits* in) {
-  return logit_rows(in) * in->vocab * dtype_bytes(static_cast<int>(in->dtype)) > kStreamBytes;
+int64_t logit_bytes(const finetune_logits* in) {
+  return logit_rows(in) * in->vocab * dtype_bytes(static_cast<int>(in->dtype));
 }
 
 // the rows' log-probabilities, or, where rows are split, their parts
@@ -214,7 +223,7 @@ int launch_rows(const finetune_logits* in, const RowSplit& split, float* logp, f
   const int64_t rows = logit_rows(in);
   if (rows == 0) return RDFFT_OK;
   by_threads(split.nt, [&](auto nt) {
-    by_stream(streams(in), [&](auto stream) {
+    by_stream(past_caches(logit_bytes(in)), [&](auto stream) {
       constexpr int NT = decltype(nt)::value;
       hipLaunchKernelGGL((token_logprob_kernel<Io, NT, decltype(stream)::value>), dim3(grid_of(rows * split.parts)),
                          dim3(NT), 0, s, rows_of<Io>(in), in->labels, logp, lse,
@@ -247,7 +256,7 @@ int launch_grad(const finetune_logits* in, const float* lse, const RowScale& sca
     using Io = decltype(io);
     const RowSplit split = row_split(in);
     by_threads(split.nt, [&](auto nt) {
-      by_stream(streams(in), [&](auto stream) {
+      by_stream(past_caches(2 * logit_bytes(in)), [&](auto stream) {
         constexpr int NT = decltype(nt)::value;
         hipLaunchKernelGGL((logits_grad_kernel<Io, NT, decltype(stream)::value>), dim3(grid_of(rows * split.parts)),
                            dim3(NT), 0, s, rows_of<Io>(in), in->labels, lse, scale, rows_of<Io>(out), rows,
@@ -369,7 +378,7 @@ int launch_policy_step(const finetune_logits* in, const PolicyCall& c, float sca
   st = by_dtype(in->dtype, [&](auto io) {
     using Io = decltype(io);
     by_held_row(in, [&](auto nt, auto r) {
-      by_stream(streams(in), [&](auto stream) {
+      by_stream(past_caches(2 * logit_bytes(in)), [&](auto stream) {
         constexpr int NT = decltype(nt)::value, R = decltype(r)::value;
         hipLaunchKernelGGL((policy_step_kernel<Io, NT, R, decltype(stream)::value>),
                            dim3(static_cast<unsigned>(logit_rows(in))), dim3(NT), 0, s, rows_of<Io>(in), in->labels,

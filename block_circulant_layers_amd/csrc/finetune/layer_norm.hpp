@@ -21,7 +21,7 @@ constexpr int kNormElems = 16;
 constexpr int norm_wg(int t) { return t > kNormThreads ? t : kNormThreads; }
 
 // RAGGED: the row's length is no multiple of a piece, so a piece may be cut.
-template <class Io, int T, bool RAGGED>
+template <class Io, int T, bool RAGGED, bool STREAM>
 struct NormRow {
   static constexpr int V = Io::kVec;
   static constexpr int E = kNormElems;
@@ -39,7 +39,7 @@ struct NormRow {
       const int c = col(i);
       raw[i] = {};
       if (c + V <= d) {
-        raw[i] = *reinterpret_cast<const typename Io::Vec*>(p + c);
+        raw[i] = load_vec<Io, STREAM>(p + c);
       } else if (RAGGED && c < d) {
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -56,7 +56,7 @@ struct NormRow {
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = Io::narrow(v[i * V + e]);
       if (c + V <= d) {
-        *reinterpret_cast<typename Io::Vec*>(p + c) = o;
+        store_vec<Io, STREAM>(p + c, o);
       } else if (RAGGED && c < d) {
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -88,11 +88,11 @@ struct NormRow {
 // the registers, not E x^2 - mean^2, which cancels for rows whose mean is
 // large against their spread.  The next row's loads are in flight while a row
 // is summed.
-template <class Io, int T, bool RAGGED>
+template <class Io, int T, bool RAGGED, bool STREAM>
 __global__ void __launch_bounds__(norm_wg(T))
     layer_norm_fwd_kernel(const typename Io::T* x, const float* w, const float* b, typename Io::T* y, float* mean,
                           float* rstd, int64_t rows, int d, int64_t xs, int64_t ys, float eps) {
-  using Row = NormRow<Io, T, RAGGED>;
+  using Row = NormRow<Io, T, RAGGED, STREAM>;
   constexpr int WG = norm_wg(T), G = WG / T, E = Row::E;
   __shared__ float s[2][WG / kWave];
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
@@ -139,12 +139,12 @@ __global__ void __launch_bounds__(norm_wg(T))
 // thread its own slots, and in fp32 load no row ahead.
 constexpr size_t norm_bwd_lds(int t) { return t > kNormThreads ? 2 * kNormElems * t * sizeof(float) : 0; }
 
-template <class Io, int T, bool RAGGED>
+template <class Io, int T, bool RAGGED, bool STREAM>
 __global__ void __launch_bounds__(norm_wg(T))
     layer_norm_bwd_kernel(const typename Io::T* x, const float* w, const float* mean, const float* rstd,
                           const typename Io::T* dy, typename Io::T* dx, float* ws, int64_t rows, int d, int64_t xs,
                           int64_t dys, int64_t dxs) {
-  using Row = NormRow<Io, T, RAGGED>;
+  using Row = NormRow<Io, T, RAGGED, STREAM>;
   constexpr int WG = norm_wg(T), G = WG / T, E = Row::E;
   __shared__ float s[2][2][WG / kWave];
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
@@ -222,12 +222,27 @@ __global__ void __launch_bounds__(norm_wg(T))
       }
     }
   } else {
+    // 16 bytes at a time where the columns are there
+    typedef float Quad __attribute__((ext_vector_type(4), aligned(4)));
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
+    for (int k = 0; k < E; k += 4) {
+      Quad q[2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        q[0][e] = IN_LDS ? mine[(k + e) * T] : dw[IN_LDS ? 0 : k + e];
+        q[1][e] = IN_LDS ? mine[(E + k + e) * T] : db[IN_LDS ? 0 : k + e];
+      }
       const int c = Row::col(k / Row::V) + k % Row::V;
-      if (c < d) {
-        slice[c] = IN_LDS ? mine[k * T] : dw[IN_LDS ? 0 : k];
-        slice[d + c] = IN_LDS ? mine[(E + k) * T] : db[IN_LDS ? 0 : k];
+      if (c + 4 <= d) {
+        *reinterpret_cast<Quad*>(slice + c) = q[0];
+        *reinterpret_cast<Quad*>(slice + d + c) = q[1];
+      } else if (RAGGED) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < d) {
+            slice[c + e] = q[0][e];
+            slice[d + c + e] = q[1][e];
+          }
       }
     }
   }
