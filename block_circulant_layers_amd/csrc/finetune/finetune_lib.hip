@@ -217,18 +217,29 @@ int64_t logit_bytes(const finetune_logits* in) {
   return logit_rows(in) * in->vocab * dtype_bytes(static_cast<int>(in->dtype));
 }
 
-// the rows' log-probabilities, or, where rows are split, their parts
+// Logits at the end of a batch that a step reads through the caches, because
+// their gradient reads them again and starts there: the size of the cache and
+// what masked rows, which are not read, leave of it.  4 x 1024 pairs of 50001
+// bf16, none / 100 / 200 / 256 / 320 / 400 / 512 MB / all of them: 366 / 358 / 352
+// / 344 / 341 / 340 / 340 / 347 us; 8 x 512 of 32768: 215 us with none, 190 us
+// with 400 MB.
+constexpr int64_t kKeepBytes = int64_t(400) << 20;
+
+// the rows' log-probabilities, or, where rows are split, their parts; `again`:
+// a gradient follows
 template <class Io>
-int launch_rows(const finetune_logits* in, const RowSplit& split, float* logp, float* lse, void* ws, hipStream_t s) {
+int launch_rows(const finetune_logits* in, const RowSplit& split, float* logp, float* lse, bool again, void* ws,
+                hipStream_t s) {
   const int64_t rows = logit_rows(in);
   if (rows == 0) return RDFFT_OK;
+  const int64_t keep = again ? std::max<int64_t>(rows - kKeepBytes / ceil_div(logit_bytes(in), rows), 0) : rows;
   by_threads(split.nt, [&](auto nt) {
     by_stream(past_caches(logit_bytes(in)), [&](auto stream) {
       constexpr int NT = decltype(nt)::value;
       hipLaunchKernelGGL((token_logprob_kernel<Io, NT, decltype(stream)::value>), dim3(grid_of(rows * split.parts)),
                          dim3(NT), 0, s, rows_of<Io>(in), in->labels, logp, lse,
                          at<float2>(ws, LogitsWorkspace(in).parts), rows, in->positions,
-                         static_cast<int>(in->vocab), split.parts, split.per);
+                         static_cast<int>(in->vocab), split.parts, split.per, keep);
     });
   });
   return launch_status();
@@ -238,7 +249,7 @@ int launch_logprob(const finetune_logits* in, float* logp, float* lse, void* ws,
   return by_dtype(in->dtype, [&](auto io) {
     using Io = decltype(io);
     const RowSplit split = row_split(in);
-    const int st = launch_rows<Io>(in, split, logp, lse, ws, s);
+    const int st = launch_rows<Io>(in, split, logp, lse, false, ws, s);
     if (st != RDFFT_OK || split.parts == 1) return st;
     const int64_t rows = logit_rows(in);
     hipLaunchKernelGGL((join_kernel<Io>), dim3(static_cast<unsigned>(ceil_div(rows, kLogitThreads))),
@@ -268,14 +279,14 @@ int launch_grad(const finetune_logits* in, const float* lse, const RowScale& sca
 }
 
 int launch_preference(const finetune_logits* in, const float* ref, const finetune_preference* how, float* loss,
-                      float* logratio, float* logp, float* lse, float* slope, void* ws, hipStream_t s) {
+                      float* logratio, float* logp, float* lse, float* slope, bool again, void* ws, hipStream_t s) {
   if (in->seqs == 0) return RDFFT_OK;
   const Preference p{static_cast<int>(how->kind), how->average != 0, how->beta, how->smoothing};
   const int64_t pairs = in->seqs / 2;
   return by_dtype(in->dtype, [&](auto io) {
     using Io = decltype(io);
     const RowSplit split = row_split(in);
-    const int st = launch_rows<Io>(in, split, logp, lse, ws, s);
+    const int st = launch_rows<Io>(in, split, logp, lse, again, ws, s);
     if (st != RDFFT_OK) return st;
     hipLaunchKernelGGL((preference_kernel<Io>), dim3(grid_of(pairs)), dim3(kLogitThreads), 0, s,
                        join_of<Io>(in, split, lse, ws), in->labels, logp, ref, p, loss, logratio, slope, pairs,
@@ -322,12 +333,12 @@ int launch_policy_sum(const finetune_logits* in, const PolicyCall& c, float* sta
 }
 
 int launch_policy(const finetune_logits* in, const PolicyCall& c, float* stats, float* logp, float* lse, float* slope,
-                  void* ws, hipStream_t s) {
+                  bool again, void* ws, hipStream_t s) {
   return by_dtype(in->dtype, [&](auto io) {
     using Io = decltype(io);
     const RowSplit split = row_split(in);
     const int64_t rows = logit_rows(in);
-    int st = launch_rows<Io>(in, split, logp, lse, ws, s);
+    int st = launch_rows<Io>(in, split, logp, lse, again, ws, s);
     if (st != RDFFT_OK) return st;
     if (rows <= kPolicyOne) {
       hipLaunchKernelGGL((policy_kernel<Io, true>), dim3(1), dim3(kPolicyThreads), 0, s,
@@ -369,7 +380,7 @@ int launch_policy_step(const finetune_logits* in, const PolicyCall& c, float sca
                        float* lse, float* slope, const finetune_dlogits* out, void* ws, hipStream_t s) {
   const bool held = by_held_row(in, [](auto, auto) {});
   if (!held) {
-    const int st = launch_policy(in, c, stats, logp, lse, slope, ws, s);
+    const int st = launch_policy(in, c, stats, logp, lse, slope, true, ws, s);
     if (st != RDFFT_OK) return st;
     return launch_grad(in, lse, RowScale{nullptr, slope, scale, 1, true}, out, s);
   }
@@ -578,7 +589,8 @@ int preference_loss_fwd(const finetune_logits* in, const float* ref_logp, const 
   const Array outs[] = {{loss, in->seqs / 2}, {logratio, in->seqs}, {logp, rows}, {lse, rows}, {slope, in->seqs}};
   if (st == RDFFT_OK) st = check_arrays(in, nullptr, ins, outs, ws, need);
   if (st != RDFFT_OK) return st;
-  return launch_preference(in, ref_logp, how, loss, logratio, logp, lse, slope, ws, static_cast<hipStream_t>(stream));
+  return launch_preference(in, ref_logp, how, loss, logratio, logp, lse, slope, false, ws,
+                           static_cast<hipStream_t>(stream));
 }
 
 int preference_loss_bwd(const finetune_logits* in, const float* lse, const float* slope, const float* dloss,
@@ -608,7 +620,7 @@ int preference_loss_step(const finetune_logits* in, const float* ref_logp, const
   if (st == RDFFT_OK) st = check_arrays(in, out, ins, outs, ws, need);
   if (st != RDFFT_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  st = launch_preference(in, ref_logp, how, loss, logratio, logp, lse, slope, ws, s);
+  st = launch_preference(in, ref_logp, how, loss, logratio, logp, lse, slope, true, ws, s);
   if (st != RDFFT_OK) return st;
   return launch_grad(in, lse, RowScale{nullptr, slope, static_cast<float>(scale), 1, false}, out, s);
 }
@@ -625,8 +637,8 @@ int policy_loss_fwd(const finetune_logits* in, const float* old_logp, const floa
   const Array outs[] = {{stats, 2}, {logp, rows}, {lse, rows}, {slope, rows}};
   if (st == RDFFT_OK) st = check_arrays(in, nullptr, ins, outs, ws, need);
   if (st != RDFFT_OK) return st;
-  return launch_policy(in, policy_call(in, old_logp, ref_logp, advantages, how, ws), stats, logp, lse, slope, ws,
-                       static_cast<hipStream_t>(stream));
+  return launch_policy(in, policy_call(in, old_logp, ref_logp, advantages, how, ws), stats, logp, lse, slope, false,
+                       ws, static_cast<hipStream_t>(stream));
 }
 
 int policy_loss_bwd(const finetune_logits* in, const float* lse, const float* slope, const float* dloss,

@@ -133,11 +133,12 @@ __device__ __forceinline__ MaxSum row_max_sum(const typename Io::T* x, int begin
 // lse and logp of every position.  One workgroup per row (parts = 1), or, where
 // there are fewer rows than the chip has room for, `parts` workgroups of `per`
 // columns each, whose maxima and sums go to `partial` for the next kernel to
-// join.
+// join.  STREAM: rows below `keep` are read past the caches, the others through
+// them.
 template <class Io, int NT, bool STREAM>
 __global__ void __launch_bounds__(NT)
     token_logprob_kernel(Rows<Io> in, const int64_t* labels, float* logp, float* lse, float2* partial, int64_t rows,
-                         int64_t positions, int v, int parts, int per) {
+                         int64_t positions, int v, int parts, int per, int64_t keep) {
   __shared__ float sm[2 * NT / kWave + 1];
   for (int64_t i = blockIdx.x; i < rows * parts; i += gridDim.x) {
     const int64_t r = parts == 1 ? i : static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(parts));
@@ -148,7 +149,8 @@ __global__ void __launch_bounds__(NT)
     }
     const typename Io::T* x = in.row(r, positions);
     const int begin = static_cast<int>(i - r * parts) * per, end = begin + per < v ? begin + per : v;
-    MaxSum a = row_max_sum<Io, NT, STREAM>(x, begin, end);
+    MaxSum a = STREAM && r < keep ? row_max_sum<Io, NT, STREAM>(x, begin, end)
+                                  : row_max_sum<Io, NT, false>(x, begin, end);
     a.template join_group<NT>(sm);
     if (threadIdx.x == 0) {
       if (parts > 1) {
@@ -240,13 +242,16 @@ struct RowScale {
   }
 };
 
-// The gradient of every row, `parts` workgroups of `per` columns a row.
+// The gradient of every row, `parts` workgroups of `per` columns a row, the
+// last row first: a step's logits were read just before, and the last of them
+// are still in the 256 MB cache.
 template <class Io, int NT, bool STREAM>
 __global__ void __launch_bounds__(NT)
     logits_grad_kernel(Rows<Io> in, const int64_t* labels, const float* lse, RowScale scale, Rows<Io> out,
                        int64_t rows, int64_t positions, int v, int parts, int per) {
   constexpr int V = Io::kVec, U = 4;
-  for (int64_t i = blockIdx.x; i < rows * parts; i += gridDim.x) {
+  for (int64_t n = blockIdx.x; n < rows * parts; n += gridDim.x) {
+    const int64_t i = rows * parts - 1 - n;
     const int64_t r = parts == 1 ? i : static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(parts));
     const int begin = static_cast<int>(i - r * parts) * per, end = begin + per < v ? begin + per : v;
     const int64_t label = labels[r];
