@@ -88,13 +88,33 @@ __device__ __forceinline__ float lanes_reduce(float v, F op) {
   return v;
 }
 
+// The same for the sum of a float, a double (its halves moved apart) or an int.
 template <int T, class V>
 __device__ __forceinline__ V lanes_sum(V v) {
   if constexpr (std::is_same_v<V, float>) {
     return lanes_reduce<T>(v, [](float a, float b) { return a + b; });
+  } else if constexpr (std::is_same_v<V, int>) {
+    return __builtin_bit_cast(int, lanes_reduce<T>(__builtin_bit_cast(float, v), [](float a, float b) {
+      return __builtin_bit_cast(float, __builtin_bit_cast(int, a) + __builtin_bit_cast(int, b));
+    }));
   } else {
-#pragma unroll
-    for (int o = T / 2; o > 0; o /= 2) v += __shfl_xor(v, o, kWave);
+    struct Halves {
+      uint32_t lo, hi;
+    };
+    const auto moved = [](V x, auto move) {
+      Halves h = __builtin_bit_cast(Halves, x);
+      return __builtin_bit_cast(V, Halves{move(h.lo), move(h.hi)});
+    };
+    if constexpr (T > 1) v += moved(v, [](uint32_t u) { return lane_swap<1>(u); });
+    if constexpr (T > 2) v += moved(v, [](uint32_t u) { return lane_swap<2>(u); });
+    if constexpr (T > 4) v += moved(v, [](uint32_t u) { return lane_swap<4>(u); });
+    if constexpr (T > 8) v += moved(v, [](uint32_t u) { return lane_swap<8>(u); });
+    if constexpr (T > 16)
+      v = moved(v, [](uint32_t u) { return __builtin_amdgcn_permlane16_swap(u, u, false, false)[0]; }) +
+          moved(v, [](uint32_t u) { return __builtin_amdgcn_permlane16_swap(u, u, false, false)[1]; });
+    if constexpr (T > 32)
+      v = moved(v, [](uint32_t u) { return __builtin_amdgcn_permlane32_swap(u, u, false, false)[0]; }) +
+          moved(v, [](uint32_t u) { return __builtin_amdgcn_permlane32_swap(u, u, false, false)[1]; });
     return v;
   }
 }

@@ -306,33 +306,50 @@ Tensor policy_loss_bwd_(const Tensor& logits, const Tensor& labels, const Tensor
 
 // ---- gradient tensors -----------------------------------------------------
 
+// the tensors of a Python list, by reference
+struct TensorList {
+  PyObject* list;
+  explicit TensorList(const py::list& l) : list(l.ptr()) {}
+  size_t size() const { return static_cast<size_t>(PyList_GET_SIZE(list)); }
+  const Tensor& operator[](size_t i) const {
+    PyObject* o = PyList_GET_ITEM(list, static_cast<Py_ssize_t>(i));
+    TORCH_CHECK_TYPE(THPVariable_Check(o), "gradients must be tensors");
+    return THPVariable_Unpack(o);
+  }
+};
+
 // max_norm absent: the norm alone.  `out` absent: in place.
-Tensor clip_grad_norm_(const std::vector<Tensor>& grads, std::optional<double> max_norm, double eps,
-                       const std::optional<std::vector<Tensor>>& out, const Opt& norm, const Opt& ws) {
-  CHECK_VALUE(!grads.empty(), "there are no gradient tensors");
+Tensor clip_grad_norm_(const py::list& grad_list, std::optional<double> max_norm, double eps,
+                       const std::optional<py::list>& out_list, const Opt& norm, const Opt& ws) {
+  const TensorList grads(grad_list);
+  CHECK_VALUE(grads.size() > 0, "there are no gradient tensors");
+  std::optional<TensorList> out;
+  if (out_list) out.emplace(*out_list);
   CHECK_VALUE(!out || out->size() == grads.size(), "out must have one tensor per gradient");
   const Tensor& first = grads[0];
   check_gpu(first);
+  const at::Device device = first.device();
   std::vector<finetune_tensor> table(grads.size());
   for (size_t i = 0; i < grads.size(); ++i) {
     const Tensor& g = grads[i];
-    CHECK_VALUE(g.layout() == at::kStrided && g.device() == first.device(),
+    CHECK_VALUE(g.layout() == at::kStrided && g.device() == device,
                 "gradients must be dense and on one GPU (there is no CPU path)");
-    CHECK_VALUE(g.is_contiguous() || g.is_non_overlapping_and_dense(),
-                "gradients must fill one block of memory each");
-    table[i] = {g.data_ptr(), g.data_ptr(), g.numel(), dtype_code(g)};
+    const bool packed = g.is_contiguous();
+    CHECK_VALUE(packed || g.is_non_overlapping_and_dense(), "gradients must fill one block of memory each");
+    table[i] = {g.data_ptr(), nullptr, g.numel(), dtype_code(g)};
+    table[i].out = const_cast<void*>(table[i].grad);
     if (out) {
       const Tensor& o = (*out)[i];
-      CHECK_VALUE(o.layout() == at::kStrided && o.device() == g.device() && o.scalar_type() == g.scalar_type() &&
-                      o.sizes() == g.sizes() && (o.strides() == g.strides() || (o.is_contiguous() && g.is_contiguous())),
+      CHECK_VALUE(o.layout() == at::kStrided && o.device() == device && o.scalar_type() == g.scalar_type() &&
+                      o.sizes() == g.sizes() && ((packed && o.is_contiguous()) || o.strides() == g.strides()),
                   "out must match the gradients in dtype, device, shape and strides");
       table[i].out = o.data_ptr();
     }
   }
   const int64_t n = static_cast<int64_t>(grads.size());
-  CHECK_VALUE(!norm || (norm->scalar_type() == at::kFloat && norm->numel() == 1 && norm->device() == first.device()),
+  CHECK_VALUE(!norm || (norm->scalar_type() == at::kFloat && norm->numel() == 1 && norm->device() == device),
               "norm must hold one float32 on the gradients' device");
-  const c10::DeviceGuard guard(first.device());
+  const c10::DeviceGuard guard(device);
   Tensor result = norm ? *norm : new_f32({}, first);
   int64_t need = 0;
   check("grad_norm_workspace", grad_norm_workspace(table.data(), n, &need));

@@ -178,9 +178,14 @@ struct JoinParts {
     double l = 0.0, p = 0.0;
     if (label >= 0 && label < v) {
       MaxSum a;
-      for (int i = 0; i < parts; ++i) {
-        const float2 q = partial[r * parts + i];
-        a.join(q.x, q.y);
+      const float2* mine = partial + r * parts;
+      for (int i = 0; i < parts; i += 8) {  // eight loads at once, then their joins
+        float2 q[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = mine[i + k < parts ? i + k : parts - 1];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i + k < parts) a.join(q[k].x, q[k].y);
       }
       l = a.lse();
       p = Io::widen(in.row(r, positions)[label]) - l;
@@ -290,40 +295,53 @@ struct Preference {
 };
 
 // One workgroup per pair: both sequences' log-ratios, the loss and the slopes.
-// The sums run in fp64 (a few values per thread).
+// The sums run in fp64 (a few values per thread), all four of them through one
+// barrier.
 template <class Io>
 __global__ void __launch_bounds__(kLogitThreads)
     preference_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, const float* ref, Preference how,
                       float* loss, float* logratio, float* slope, int64_t pairs, int64_t positions) {
-  __shared__ double s[2][kLogitThreads / kWave];
-  __shared__ double n[2][kLogitThreads / kWave];
+  constexpr int W = kLogitThreads / kWave;
+  __shared__ double s[4][W];
   for (int64_t b = blockIdx.x; b < pairs; b += gridDim.x) {
-    double ratio[2], count[2];
+    double sum[4] = {};  // log-ratio and count of the chosen sequence, then of the rejected one
+    for (int64_t i = threadIdx.x; i < positions; i += kLogitThreads) {
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const int64_t base = (b + side * pairs) * positions;
-      double a = 0.0, c = 0.0;
-      for (int64_t i = threadIdx.x; i < positions; i += kLogitThreads) {
-        const int64_t label = labels[base + i];
-        const double p = join(base + i, label, positions, logp);
+      for (int side = 0; side < 2; ++side) {
+        const int64_t r = (b + side * pairs) * positions + i, label = labels[r];
+        const double p = join(r, label, positions, logp), q = ref[r];
         if (label != kIgnore) {
-          a += p - static_cast<double>(ref[base + i]);
-          c += 1.0;
+          sum[2 * side] += p - q;
+          sum[2 * side + 1] += 1.0;
         }
       }
-      a = block_sum<kLogitThreads>(a, s[side]);
-      c = block_sum<kLogitThreads>(c, n[side]);
-      count[side] = how.average && c > 0.0 ? c : 1.0;
-      ratio[side] = a / count[side];
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      sum[k] = lanes_sum<kWave>(sum[k]);
+      if (threadIdx.x % kWave == 0) s[k][threadIdx.x / kWave] = sum[k];
+    }
+    __syncthreads();
     if (threadIdx.x == 0) {
+      double ratio[2], count[2];
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        double a = 0.0, c = 0.0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          a += s[2 * side][w];
+          c += s[2 * side + 1][w];
+        }
+        count[side] = how.average && c > 0.0 ? c : 1.0;
+        ratio[side] = a / count[side];
+      }
       const double h = ratio[0] - ratio[1], z = how.beta * h, e = how.smoothing;
       double l, dh;
       if (how.kind == 0) {
-        const double t = log1p(exp(-fabs(z)));
-        const double up = (z < 0.0 ? z : 0.0) - t;  // log sigma(z); log sigma(-z) = up - z
+        const double t = exp(-fabs(z)), up = (z < 0.0 ? z : 0.0) - log1p(t);  // log sigma(z); log sigma(-z) = up - z
+        const double big = 1.0 / (1.0 + t), small = t * big;                  // sigma(|z|) and sigma(-|z|)
         l = -(1.0 - e) * up - e * (up - z);
-        dh = -how.beta * ((1.0 - e) / (1.0 + exp(z)) - e / (1.0 + exp(-z)));
+        dh = z < 0.0 ? -how.beta * ((1.0 - e) * big - e * small) : -how.beta * ((1.0 - e) * small - e * big);
       } else if (how.kind == 1) {
         l = z < 1.0 ? 1.0 - z : z >= 1.0 ? 0.0 : z;  // the last: NaN
         dh = z < 1.0 ? -how.beta : z >= 1.0 ? 0.0 : z;
