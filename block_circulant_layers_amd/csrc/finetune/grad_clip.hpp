@@ -12,24 +12,34 @@
 namespace finetune {
 
 constexpr int kClipThreads = 256;
-constexpr int kClipChunk = 4096;    // elements of one unit of work
-constexpr int kClipTensors = 144;   // tensors of one launch (the table travels in the kernel's arguments)
+constexpr int kClipBytes = 16384;   // of a chunk, the unit of work: four 16-byte pieces a thread
+constexpr int kClipPieces = kClipBytes / 16 / kClipThreads;
+constexpr int kClipTensors = 128;   // tensors of one launch (the table travels in the kernel's arguments)
 constexpr int kClipGroups = 2048;   // workgroups of a launch at most: 8 a compute unit, and one partial sum each
+constexpr int kClipLine = 128;      // chunks start at addresses divisible by this
 
 struct ClipTable {
   const void* in[kClipTensors];
   void* out[kClipTensors];
-  int last[kClipTensors];           // elements of each tensor's last chunk; 2 bits of type above them
-  int first[kClipTensors + 1];      // first chunk of each tensor within the launch
+  int64_t count[kClipTensors];
+  int first[kClipTensors + 1];  // first chunk of each tensor within the launch
+  int8_t dtype[kClipTensors];
   int n;
 };
-static_assert(sizeof(ClipTable) <= 3600, "kernel arguments are limited to 4 KB");
-constexpr int kClipTypeShift = 16;
-static_assert(kClipChunk < 1 << kClipTypeShift);
+static_assert(sizeof(ClipTable) <= 3800, "kernel arguments are limited to 4 KB");
 
-// The tensor that chunk c belongs to: the last whose first chunk is <= c.
-__device__ __forceinline__ int tensor_of(const ClipTable& t, int c) {
-  int lo = 0, hi = t.n;
+// Elements between the last 128-byte line before p and p: chunk k of a tensor
+// holds its elements [k N - lead, (k + 1) N - lead), N = 16 KB of them, so that
+// every chunk but the first starts on a line.
+__host__ __device__ inline int clip_lead(const void* p, int size) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) % kClipLine) / size;
+}
+
+// The tensor that chunk c belongs to, at or after tensor i: the last whose
+// first chunk is <= c.
+__device__ __forceinline__ int tensor_of(const ClipTable& t, int c, int i) {
+  if (c < t.first[i + 1]) return i;
+  int lo = i + 1, hi = t.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (t.first[mid] <= c)
@@ -40,82 +50,82 @@ __device__ __forceinline__ int tensor_of(const ClipTable& t, int c) {
   return lo;
 }
 
-// This workgroup's share of the launch: consecutive chunks, as one run a tensor
-// they touch.  f(storage type, pointer in, pointer out, elements) for every run,
-// the last one first if BACK.  (Single chunks dealt out in turn took 533 us where
-// runs take TBD us: every chunk waited for its table entries.)
-template <bool BACK, class F>
-__device__ __forceinline__ void for_runs(const ClipTable& t, F f) {
-  const int chunks = t.first[t.n], per = (chunks + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-  int c0 = static_cast<int>(blockIdx.x) * per, c1 = c0 + per < chunks ? c0 + per : chunks;
-  if (c0 >= c1) return;
-  for (int i = tensor_of(t, BACK ? c1 - 1 : c0); c0 < c1; i += BACK ? -1 : 1) {
-    const int from = t.first[i], to = t.first[i + 1], last = t.last[i];
-    const int a = from > c0 ? from : c0, b = to < c1 ? to : c1;
-    const int64_t begin = static_cast<int64_t>(a - from) * kClipChunk;
-    const int n = (b - a) * kClipChunk - (b == to ? kClipChunk - (last & ((1 << kClipTypeShift) - 1)) : 0);
+// f(storage type, tensor's pointer in, out, begin, end) for every chunk of this
+// workgroup, dealt out in turn so that all workgroups read one region at a
+// time.  BACK: a tensor's last chunk first.  `at` of a tensor is the pointer
+// whose lines the chunks follow.
+template <bool BACK, class At, class F>
+__device__ __forceinline__ void for_chunks(const ClipTable& t, At at, F f) {
+  const int chunks = t.first[t.n];
+  int i = 0;
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    i = tensor_of(t, c, i);
     const auto with = [&](auto io) {
       using T = typename decltype(io)::T;
-      f(io, static_cast<const T*>(t.in[i]) + begin, static_cast<T*>(t.out[i]) + begin, n);
+      constexpr int N = kClipBytes / sizeof(T);
+      const int64_t k = BACK ? t.first[i + 1] - 1 - c : c - t.first[i];
+      const int64_t a = k * N - clip_lead(at(i), sizeof(T)), b = a + N, n = t.count[i];
+      f(io, static_cast<const T*>(t.in[i]), static_cast<T*>(t.out[i]), a > 0 ? a : 0, b < n ? b : n, a, c);
     };
-    const int type = last >> kClipTypeShift;
-    if (type == 0)
+    if (t.dtype[i] == 0)
       with(F32{});
-    else if (type == 1)
+    else if (t.dtype[i] == 1)
       with(Bf16{});
     else
       with(F16{});
-    if (BACK)
-      c1 = a;
-    else
-      c0 = b;
   }
 }
 
-// g(column, piece or single value) over n elements at p: batches of U pieces a
-// thread, the last batch first if BACK
-template <class Io, int U, bool BACK, class Batch, class Piece, class One>
-__device__ __forceinline__ void for_pieces(const typename Io::T* at, int n, Batch batch, Piece piece, One one) {
-  constexpr int V = Io::kVec, STEP = U * kClipThreads * V;
-  const Pieces<Io> p(at, 0, n);
-  const int t = p.first + static_cast<int>(threadIdx.x) * V, full = (p.last - p.first) / STEP;
-  const auto rest = [&]() {
-    for (int j = t + full * STEP; j < p.last; j += kClipThreads * V) piece(j);
-    p.template rest<kClipThreads>(one);
-  };
-  if (BACK) rest();
-  for (int k = 0; k < full; ++k) batch(t + (BACK ? full - 1 - k : k) * STEP);
-  if (!BACK) rest();
+// A chunk [begin, end) of a tensor whose lines start at `origin` (at or before
+// begin): piece(slot, column) for the thread's whole 16-byte pieces, then
+// one(column) for the columns that a cut first or last piece leaves.
+template <class Io, class Piece, class One>
+__device__ __forceinline__ void for_pieces(int64_t origin, int64_t begin, int64_t end, Piece piece, One one) {
+  constexpr int V = Io::kVec;
+  const int head = static_cast<int>(begin - origin) % V;  // columns missing from the first piece
+  const int64_t first = begin + (head ? V - head : 0), last = first < end ? first + (end - first) / V * V : first;
+#pragma unroll
+  for (int u = 0; u < kClipPieces; ++u) {
+    const int64_t j = origin + (u * kClipThreads + static_cast<int>(threadIdx.x)) * V;
+    if (j >= first && j < last) piece(u, j);
+  }
+  const int t = threadIdx.x, before = static_cast<int>((first < end ? first : end) - begin);
+  if (t < before)
+    one(begin + t);
+  else if (last + t - before < end && last >= first && first < end)
+    one(last + t - before);
 }
 
-// partial[workgroup] = the sum of squares of the chunks it walks over
-__global__ void __launch_bounds__(kClipThreads) grad_square_kernel(ClipTable t, double* partial) {
+// partial[workgroup] = the sum of squares of its chunks; those below `keep` are
+// read past the caches
+__global__ void __launch_bounds__(kClipThreads) grad_square_kernel(ClipTable t, int keep, double* partial) {
   __shared__ double s[kClipThreads / kWave];
-  double a[2] = {0.0, 0.0};
-  for_runs<false>(t, [&](auto io, const auto* g, auto*, int n) {
-    using Io = decltype(io);
-    constexpr int V = Io::kVec, U = 8;
-    const auto add = [&](auto v, int k) {
-      const double x = Io::widen(v);
-      a[k % 2] = __builtin_fma(x, x, a[k % 2]);
-    };
-    for_pieces<Io, U, false>(
-        g, n,
-        [&](int j) {
-          typename Io::Vec raw[U];
+  double sum[2] = {0.0, 0.0};
+  for_chunks<false>(
+      t, [&](int i) { return t.in[i]; },
+      [&](auto io, const auto* g, auto*, int64_t begin, int64_t end, int64_t origin, int c) {
+        using Io = decltype(io);
+        constexpr int V = Io::kVec;
+        typename Io::Vec raw[kClipPieces] = {};  // pieces that are not there add zero
+        typename Io::T single = 0;
+        const auto load = [&](auto stream) {
+          for_pieces<Io>(
+              origin, begin, end, [&](int u, int64_t j) { raw[u] = load_vec<Io, decltype(stream)::value>(g + j); },
+              [&](int64_t j) { single = g[j]; });
+        };
+        if (c < keep)
+          load(std::true_type{});
+        else
+          load(std::false_type{});
+        const auto add = [&](auto v, int k) {
+          const double x = Io::widen(v);
+          sum[k % 2] = __builtin_fma(x, x, sum[k % 2]);
+        };
 #pragma unroll
-          for (int u = 0; u < U; ++u) raw[u] = load_vec<Io>(g + j + u * kClipThreads * V);
-#pragma unroll
-          for (int k = 0; k < U * V; ++k) add(raw[k / V][k % V], k);
-        },
-        [&](int j) {
-          const typename Io::Vec raw = load_vec<Io>(g + j);
-#pragma unroll
-          for (int k = 0; k < V; ++k) add(raw[k], k);
-        },
-        [&](int i) { add(g[i], 0); });
-  });
-  const double all = block_sum<kClipThreads>(a[0] + a[1], s);
+        for (int k = 0; k < kClipPieces * V; ++k) add(raw[k / V][k % V], k);
+        add(single, 0);
+      });
+  const double all = block_sum<kClipThreads>(sum[0] + sum[1], s);
   if (threadIdx.x == 0) partial[blockIdx.x] = all;
 }
 
@@ -135,8 +145,9 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const double* p
 
 // out = g min(1, max / (norm + eps)).  Every workgroup sums the partial sums
 // itself (16 KB from L2 at most a launch of squares) instead of waiting for a
-// kernel that does, and goes through its share backwards: what the squares
-// read last is still in the 256 MB cache.
+// kernel that does.  The tables come in reverse and so do a tensor's chunks:
+// what the squares read last is still in the 256 MB cache.
+template <bool STREAM>
 __global__ void __launch_bounds__(kClipThreads)
     grad_scale_kernel(ClipTable t, const double* partial, int64_t parts, double max_norm, double eps, float* norm) {
   __shared__ double s[kClipThreads / kWave];
@@ -144,27 +155,24 @@ __global__ void __launch_bounds__(kClipThreads)
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = static_cast<float>(a);
   const double q = max_norm / (a + eps);
   const float f = q > 1.0 ? 1.0f : static_cast<float>(q);
-  for_runs<true>(t, [&](auto io, const auto* g, auto* o, int n) {
-    using Io = decltype(io);
-    constexpr int V = Io::kVec, U = 4;
-    if (f == 1.0f && g == o) return;  // nothing to change in place
-    const auto scaled = [&](typename Io::Vec v) {
+  for_chunks<true>(
+      t, [&](int i) { return static_cast<const void*>(t.out[i]); },
+      [&](auto io, const auto* g, auto* o, int64_t begin, int64_t end, int64_t origin, int) {
+        using Io = decltype(io);
+        constexpr int V = Io::kVec;
+        if (f == 1.0f && g == o) return;  // nothing to change in place
+        typename Io::Vec raw[kClipPieces];
+        for_pieces<Io>(
+            origin, begin, end, [&](int u, int64_t j) { raw[u] = load_vec<Io, STREAM>(g + j); }, [](int64_t) {});
+        for_pieces<Io>(
+            origin, begin, end,
+            [&](int u, int64_t j) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[k] = Io::narrow(Io::widen(v[k]) * f);
-      return v;
-    };
-    for_pieces<Io, U, true>(
-        o, n,
-        [&](int j) {
-          typename Io::Vec raw[U];
-#pragma unroll
-          for (int u = 0; u < U; ++u) raw[u] = load_vec<Io>(g + j + u * kClipThreads * V);
-#pragma unroll
-          for (int u = 0; u < U; ++u) store_vec<Io>(o + j + u * kClipThreads * V, scaled(raw[u]));
-        },
-        [&](int j) { store_vec<Io>(o + j, scaled(load_vec<Io>(g + j))); },
-        [&](int i) { o[i] = Io::narrow(Io::widen(g[i]) * f); });
-  });
+              for (int k = 0; k < V; ++k) raw[u][k] = Io::narrow(Io::widen(raw[u][k]) * f);
+              store_vec<Io, STREAM>(o + j, raw[u]);
+            },
+            [&](int64_t j) { o[j] = Io::narrow(Io::widen(g[j]) * f); });
+      });
 }
 
 }  // namespace finetune

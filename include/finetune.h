@@ -223,7 +223,7 @@ typedef struct {
   int64_t dtype;
 } finetune_tensor;
 
-/* Bytes of the workspace of grad_norm and clip_grad_norm for these counts. */
+/* Bytes of the workspace of grad_norm and clip_grad_norm for these tensors (`out` unread). */
 int grad_norm_workspace(const finetune_tensor* tensors, int64_t n, int64_t* bytes);
 
 /* grad_norm -- norm[0] = sqrt(sum of g^2 over all tensors) (`out` unread). */
