@@ -159,9 +159,16 @@ Rows<Io> rows_of(const finetune_dlogits* out) {
 
 // How a launch over rows of `vocab` columns is split: `nt` threads a
 // workgroup, `parts` workgroups of `per` columns a row.  A row of up to four
-// pieces a lane takes one wave.  Fewer rows than kWantGroups workgroups are
-// split until there are as many, or until a part holds one piece a thread.
-constexpr int64_t kWantGroups = 1024;
+// pieces a lane takes one wave.  Fewer rows than kWantGroups workgroups, two a
+// compute unit, are split until there are as many, or until a part holds one
+// piece a thread.  (With 1024 as the limit, 999 rows of 10007 fp32 took 15.1 us
+// in two parts each and their joins, 13.4 us whole; a step of 512 rows of 50001
+// bf16 31 us in parts, 27 us with the rows held.)
+// (A host build that runs the kernels on CPU threads wants fewer.)
+#ifndef FINETUNE_WANT_GROUPS
+#define FINETUNE_WANT_GROUPS 512
+#endif
+constexpr int64_t kWantGroups = FINETUNE_WANT_GROUPS;
 struct RowSplit {
   int nt, parts, per;
 };
@@ -209,8 +216,10 @@ T* at(void* ws, int64_t offset) {
 
 template <class Io>
 JoinParts<Io> join_of(const finetune_logits* in, const RowSplit& split, float* lse, void* ws) {
+  int lanes = 1;
+  while (lanes < split.parts && lanes < kWave) lanes *= 2;
   return {rows_of<Io>(in), split.parts > 1 ? at<const float2>(ws, LogitsWorkspace(in).parts) : nullptr, lse, split.parts,
-          static_cast<int>(in->vocab)};
+          lanes, static_cast<int>(in->vocab)};
 }
 
 int64_t logit_bytes(const finetune_logits* in) {
@@ -252,8 +261,8 @@ int launch_logprob(const finetune_logits* in, float* logp, float* lse, void* ws,
     const int st = launch_rows<Io>(in, split, logp, lse, false, ws, s);
     if (st != RDFFT_OK || split.parts == 1) return st;
     const int64_t rows = logit_rows(in);
-    hipLaunchKernelGGL((join_kernel<Io>), dim3(static_cast<unsigned>(ceil_div(rows, kLogitThreads))),
-                       dim3(kLogitThreads), 0, s, join_of<Io>(in, split, lse, ws), in->labels, logp, rows,
+    hipLaunchKernelGGL((join_kernel<Io>), dim3(static_cast<unsigned>(ceil_div(rows, kJoinRows))), dim3(kLogitThreads),
+                       0, s, join_of<Io>(in, split, lse, ws), in->labels, logp, rows,
                        in->positions);
     return launch_status();
   });
@@ -298,6 +307,7 @@ int launch_preference(const finetune_logits* in, const float* ref, const finetun
 // Rows up to which one workgroup does all that follows the log-probabilities
 // (8192 rows took one workgroup 32 us, three launches 13 us).
 constexpr int64_t kPolicyOne = 2048;
+static_assert(kPolicyOne >= kWantGroups, "rows in parts are joined by that workgroup");
 
 // what policy kernels share
 struct PolicyCall {

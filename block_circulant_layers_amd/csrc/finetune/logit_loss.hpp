@@ -165,44 +165,51 @@ __global__ void __launch_bounds__(NT)
   }
 }
 
-// The positions' lse and logp from their parts, one thread a row.
+// The positions' lse and logp from their parts.
 template <class Io>
 struct JoinParts {
   Rows<Io> in;
   const float2* partial;  // null: logp and lse are there already
   float* lse;
-  int parts, v;
-  // logp of row r (and, joined here, its lse stored)
-  __device__ __forceinline__ float operator()(int64_t r, int64_t label, int64_t positions, float* logp) const {
-    if (!partial) return logp[r];
-    double l = 0.0, p = 0.0;
-    if (label >= 0 && label < v) {
+  int parts, lanes, v;  // lanes: of one row, a power of two up to 64
+
+  // Rows [first, first + count) by the NT threads of a workgroup, `lanes` of
+  // them a row; all of its threads have the results after the barrier at the
+  // end.  (One thread a row took 8.6 us for the 64 parts of a single row.)
+  template <int NT>
+  __device__ __forceinline__ void operator()(int64_t first, int64_t count, const int64_t* labels, int64_t positions,
+                                             float* logp) const {
+    if (!partial) return;
+    const int lane = static_cast<int>(threadIdx.x) & (lanes - 1), at_once = NT / lanes;
+    for (int64_t base = 0; base < count; base += at_once) {
+      const int64_t i = base + static_cast<int>(threadIdx.x) / lanes, r = first + i;
+      const int64_t label = i < count ? labels[r] : kIgnore;
+      const bool known = label >= 0 && label < v;
       MaxSum a;
-      const float2* mine = partial + r * parts;
-      for (int i = 0; i < parts; i += 8) {  // eight loads at once, then their joins
-        float2 q[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) q[k] = mine[i + k < parts ? i + k : parts - 1];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (i + k < parts) a.join(q[k].x, q[k].y);
+      if (known)
+        for (int k = lane; k < parts; k += lanes) {
+          const float2 q = partial[r * parts + k];
+          a.join(q.x, q.y);
+        }
+      for (int o = lanes / 2; o > 0; o /= 2) a.join(__shfl_xor(a.m, o, kWave), __shfl_xor(a.s, o, kWave));
+      if (lane == 0 && i < count) {
+        const double l = known ? a.lse() : label == kIgnore ? 0.0 : NAN;
+        lse[r] = static_cast<float>(l);
+        logp[r] = static_cast<float>(known ? Io::widen(in.row(r, positions)[label]) - l : l);
       }
-      l = a.lse();
-      p = Io::widen(in.row(r, positions)[label]) - l;
-    } else if (label != kIgnore) {
-      l = p = NAN;
     }
-    lse[r] = static_cast<float>(l);
-    return logp[r] = static_cast<float>(p);
+    __syncthreads();
   }
 };
 
 // ... for a caller that wants nothing but the log-probabilities
+constexpr int kJoinRows = 64;  // of a workgroup
 template <class Io>
 __global__ void __launch_bounds__(kLogitThreads)
     join_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, int64_t rows, int64_t positions) {
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * kLogitThreads + threadIdx.x;
-  if (r < rows) join(r, labels[r], positions, logp);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kJoinRows;
+  join.template operator()<kLogitThreads>(first, rows - first < kJoinRows ? rows - first : kJoinRows, labels,
+                                          positions, logp);
 }
 
 // One row's gradient g (1[j = label] - exp(x_j - lse)): with L = log2(e),
@@ -304,12 +311,14 @@ __global__ void __launch_bounds__(kLogitThreads)
   constexpr int W = kLogitThreads / kWave;
   __shared__ double s[4][W];
   for (int64_t b = blockIdx.x; b < pairs; b += gridDim.x) {
+    for (int side = 0; side < 2; ++side)
+      join.template operator()<kLogitThreads>((b + side * pairs) * positions, positions, labels, positions, logp);
     double sum[4] = {};  // log-ratio and count of the chosen sequence, then of the rejected one
     for (int64_t i = threadIdx.x; i < positions; i += kLogitThreads) {
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
         const int64_t r = (b + side * pairs) * positions + i, label = labels[r];
-        const double p = join(r, label, positions, logp), q = ref[r];
+        const double p = logp[r], q = ref[r];
         if (label != kIgnore) {
           sum[2 * side] += p - q;
           sum[2 * side + 1] += 1.0;
@@ -449,13 +458,14 @@ __global__ void __launch_bounds__(ONE ? kPolicyThreads : kLogitThreads)
   __shared__ int sc[NT / kWave];
   if constexpr (ONE) {
     policy_counts(labels, counts, total, how.reduction, seqs, positions, sc);
+    join.template operator()<NT>(0, seqs * positions, labels, positions, logp);
     __syncthreads();
   }
   const uint32_t rows = static_cast<uint32_t>(seqs * positions), n = static_cast<uint32_t>(positions);
   double a = 0.0, k = 0.0;
   for (uint32_t r = blockIdx.x * NT + threadIdx.x; r < rows; r += gridDim.x * NT) {
     const int64_t label = labels[r];
-    const float p = join(r, label, positions, logp);
+    const float p = logp[r];  // (rows in parts are few: they come with ONE)
     double2 t = make_double2(0.0, 0.0);
     float g = 0.0f;
     if (label != kIgnore) {
