@@ -64,6 +64,22 @@ float* f32(const char* name, const Opt& t, at::IntArrayRef shape, const Tensor& 
 
 Tensor new_f32(at::IntArrayRef shape, const Tensor& like) { return at::empty(shape, like.options().dtype(at::kFloat)); }
 
+// Several small arrays of one call in one allocation: each an allocation of its
+// own costs the host 0.8 us, one of 13 us in a loss step of a few kilobytes.
+struct Block {
+  Tensor t;
+  int64_t used = 0;
+  Block(const Tensor& like, int64_t floats) : t(at::empty({floats}, like.options().dtype(at::kFloat))) {}
+  // the next array: a tensor on the block's storage
+  Tensor next(at::IntArrayRef shape) {
+    auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
+    impl->set_storage_offset(t.storage_offset() + used);
+    impl->set_sizes_contiguous(shape);
+    used += impl->numel();
+    return Tensor(std::move(impl));
+  }
+};
+
 // the caller's workspace or a new one
 struct Workspace {
   Tensor t;
@@ -76,6 +92,8 @@ struct Workspace {
       t = at::empty({bytes}, like.options().dtype(at::kByte));
     }
   }
+  // the first `need` bytes of a block, whose arrays follow
+  Workspace(Block& block, int64_t need) : t(block.next({need / 4})) {}
   void* p() const { return t.data_ptr(); }
   int64_t bytes() const { return t.numel() * t.element_size(); }
 };
@@ -120,7 +138,8 @@ std::tuple<Tensor, Tensor, Tensor> layer_norm_fwd_(const Tensor& x, const Opt& w
   const c10::DeviceGuard guard(x.device());
   Tensor out = y ? *y : at::empty(x.sizes(), x.options());
   const auto lead = x.sizes().slice(0, x.dim() - 1);
-  Tensor mean = new_f32(lead, x), rstd = new_f32(lead, x);
+  Block block(x, 2 * r.rows);
+  Tensor mean = block.next(lead), rstd = block.next(lead);
   check("layer_norm_fwd",
         layer_norm_fwd(x.data_ptr(), w, b, out.data_ptr(), static_cast<float*>(mean.data_ptr()),
                        static_cast<float*>(rstd.data_ptr()), r.rows, r.d, r.stride, ys, eps, code, stream_of(x)));
@@ -188,19 +207,32 @@ Tensor dlogits_of(const Tensor& logits, const Opt& out) {
 }
 finetune_dlogits dlogits_args(const Tensor& out) { return {out.data_ptr(), out.stride(0), out.stride(1)}; }
 
-Workspace logits_workspace(const Tensor& logits, const finetune_logits& in, const Opt& ws) {
-  int64_t need = 0;
-  check("finetune_logits_workspace", finetune_logits_workspace(&in, &need));
-  return Workspace(logits, need, ws);
-}
+// the workspace and `floats` of outputs behind it in one block, or the caller's workspace
+struct LogitsBlock {
+  Block block;
+  Workspace work;
+  LogitsBlock(const Tensor& logits, const finetune_logits& in, int64_t floats, const Opt& ws)
+      : LogitsBlock(logits, ws ? 0 : need_of(in), floats, ws) {}
+  Tensor next(at::IntArrayRef shape) { return block.next(shape); }
+
+ private:
+  LogitsBlock(const Tensor& logits, int64_t need, int64_t floats, const Opt& ws)
+      : block(logits, need / 4 + floats), work(ws ? Workspace(logits, 0, ws) : Workspace(block, need)) {}
+  static int64_t need_of(const finetune_logits& in) {
+    int64_t need = 0;
+    check("finetune_logits_workspace", finetune_logits_workspace(&in, &need));
+    return need;
+  }
+};
 
 float* ptr(const Tensor& t) { return static_cast<float*>(t.data_ptr()); }
 
 std::tuple<Tensor, Tensor> token_logprob_(const Tensor& logits, const Tensor& labels, const Opt& ws) {
   const finetune_logits in = logits_of(logits, labels);
   const c10::DeviceGuard guard(logits.device());
-  Tensor logp = new_f32(labels.sizes(), logits), lse = new_f32(labels.sizes(), logits);
-  const Workspace work = logits_workspace(logits, in, ws);
+  LogitsBlock block(logits, in, 2 * in.seqs * in.positions, ws);
+  const Workspace& work = block.work;
+  Tensor logp = block.next(labels.sizes()), lse = block.next(labels.sizes());
   check("token_logprob", token_logprob(&in, ptr(logp), ptr(lse), work.p(), work.bytes(), stream_of(logits)));
   return {logp, lse};
 }
@@ -226,11 +258,11 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor, Opt> preference_loss_(
   const float* ref = f32("ref_logp", ref_logp, labels.sizes(), logits);
   check_dlogits(logits, dlogits);
   const c10::DeviceGuard guard(logits.device());
-  Tensor loss = new_f32({in.seqs / 2}, logits), ratio = new_f32({in.seqs}, logits),
-         logp = new_f32(labels.sizes(), logits), lse = new_f32(labels.sizes(), logits),
-         slope = new_f32({in.seqs}, logits);
+  LogitsBlock block(logits, in, in.seqs / 2 + 2 * in.seqs + 2 * in.seqs * in.positions, ws);
+  const Workspace& work = block.work;
+  Tensor loss = block.next({in.seqs / 2}), ratio = block.next({in.seqs}), logp = block.next(labels.sizes()),
+         lse = block.next(labels.sizes()), slope = block.next({in.seqs});
   const finetune_preference how{kind, average, beta, smoothing};
-  const Workspace work = logits_workspace(logits, in, ws);
   if (!scale) {
     check("preference_loss_fwd", preference_loss_fwd(&in, ref, &how, ptr(loss), ptr(ratio), ptr(logp), ptr(lse),
                                                      ptr(slope), work.p(), work.bytes(), stream_of(logits)));
@@ -272,20 +304,20 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor, Opt> policy_loss_(
   const float* adv = f32("advantages", advantages, advantages.sizes(), logits);
   check_dlogits(logits, dlogits);
   const c10::DeviceGuard guard(logits.device());
-  Tensor stats = new_f32({2}, logits), logp = new_f32(labels.sizes(), logits), lse = new_f32(labels.sizes(), logits),
-         slope = new_f32(labels.sizes(), logits);
+  LogitsBlock block(logits, in, 2 + 3 * in.seqs * in.positions, ws);
+  const Workspace& work = block.work;
+  Tensor loss = block.next({}), kl = block.next({}), logp = block.next(labels.sizes()),
+         lse = block.next(labels.sizes()), slope = block.next(labels.sizes());
   const finetune_policy how{reduction, per_token, clip_low, clip_high, kl_coef};
-  const Workspace work = logits_workspace(logits, in, ws);
-  Tensor loss = stats.select(0, 0), kl = stats.select(0, 1);
   if (!scale) {
-    check("policy_loss_fwd", policy_loss_fwd(&in, old, ref, adv, &how, ptr(stats), ptr(logp), ptr(lse), ptr(slope),
+    check("policy_loss_fwd", policy_loss_fwd(&in, old, ref, adv, &how, ptr(loss), ptr(logp), ptr(lse), ptr(slope),
                                              work.p(), work.bytes(), stream_of(logits)));
     return {loss, kl, logp, lse, slope, std::nullopt};
   }
   Tensor out = dlogits_of(logits, dlogits);
   const finetune_dlogits args = dlogits_args(out);
   check("policy_loss_step",
-        policy_loss_step(&in, old, ref, adv, &how, *scale, ptr(stats), ptr(logp), ptr(lse), ptr(slope), &args,
+        policy_loss_step(&in, old, ref, adv, &how, *scale, ptr(loss), ptr(logp), ptr(lse), ptr(slope), &args,
                          work.p(), work.bytes(), stream_of(logits)));
   return {loss, kl, logp, lse, slope, out};
 }
