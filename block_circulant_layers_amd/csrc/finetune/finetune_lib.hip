@@ -196,16 +196,17 @@ void by_threads(int nt, F f) {
 
 // Workspace of the calls on logits: one total, a count a sequence, two fp64
 // shares a row (policy loss), and the parts of split rows (a maximum and a sum
-// each).
+// each) with their labels' logits.
 struct LogitsWorkspace {
-  int64_t counts, terms, parts, bytes;  // offsets, and the size
+  int64_t counts, terms, parts, picked, bytes;  // offsets, and the size
   explicit LogitsWorkspace(const finetune_logits* in) {
     const auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
     const RowSplit s = row_split(in);
     counts = 16;
     terms = counts + up(in->seqs * 4);
     parts = terms + logit_rows(in) * 16;
-    bytes = parts + (s.parts > 1 ? up(logit_rows(in) * s.parts * 8) : 0);
+    picked = parts + (s.parts > 1 ? up(logit_rows(in) * s.parts * 8) : 0);
+    bytes = picked + (s.parts > 1 ? up(logit_rows(in) * 4) : 0);
   }
 };
 int64_t logits_workspace(const finetune_logits* in) { return LogitsWorkspace(in).bytes; }
@@ -218,8 +219,8 @@ template <class Io>
 JoinParts<Io> join_of(const finetune_logits* in, const RowSplit& split, float* lse, void* ws) {
   int lanes = 1;
   while (lanes < split.parts && lanes < kWave) lanes *= 2;
-  return {rows_of<Io>(in), split.parts > 1 ? at<const float2>(ws, LogitsWorkspace(in).parts) : nullptr, lse, split.parts,
-          lanes, static_cast<int>(in->vocab)};
+  return {rows_of<Io>(in), split.parts > 1 ? at<const float2>(ws, LogitsWorkspace(in).parts) : nullptr,
+          at<const float>(ws, LogitsWorkspace(in).picked), lse, split.parts, lanes, static_cast<int>(in->vocab)};
 }
 
 int64_t logit_bytes(const finetune_logits* in) {
@@ -247,7 +248,8 @@ int launch_rows(const finetune_logits* in, const RowSplit& split, float* logp, f
       constexpr int NT = decltype(nt)::value;
       hipLaunchKernelGGL((token_logprob_kernel<Io, NT, decltype(stream)::value>), dim3(grid_of(rows * split.parts)),
                          dim3(NT), 0, s, rows_of<Io>(in), in->labels, logp, lse,
-                         at<float2>(ws, LogitsWorkspace(in).parts), rows, in->positions,
+                         at<float2>(ws, LogitsWorkspace(in).parts), at<float>(ws, LogitsWorkspace(in).picked), rows,
+                         in->positions,
                          static_cast<int>(in->vocab), split.parts, split.per, keep);
     });
   });
@@ -262,8 +264,7 @@ int launch_logprob(const finetune_logits* in, float* logp, float* lse, void* ws,
     if (st != RDFFT_OK || split.parts == 1) return st;
     const int64_t rows = logit_rows(in);
     hipLaunchKernelGGL((join_kernel<Io>), dim3(static_cast<unsigned>(ceil_div(rows, kJoinRows))), dim3(kLogitThreads),
-                       0, s, join_of<Io>(in, split, lse, ws), in->labels, logp, rows,
-                       in->positions);
+                       0, s, join_of<Io>(in, split, lse, ws), in->labels, logp, rows);
     return launch_status();
   });
 }
@@ -287,10 +288,13 @@ int launch_grad(const finetune_logits* in, const float* lse, const RowScale& sca
   });
 }
 
-int launch_preference(const finetune_logits* in, const float* ref, const finetune_preference* how, float* loss,
-                      float* logratio, float* logp, float* lse, float* slope, bool again, void* ws, hipStream_t s) {
+Preference preference_of(const finetune_preference* how) {
+  return {static_cast<int>(how->kind), how->average != 0, how->beta, how->smoothing};
+}
+
+int launch_preference(const finetune_logits* in, const float* ref, const finetune_preference* how,
+                      const PreferenceOut& res, float* logp, float* lse, bool again, void* ws, hipStream_t s) {
   if (in->seqs == 0) return RDFFT_OK;
-  const Preference p{static_cast<int>(how->kind), how->average != 0, how->beta, how->smoothing};
   const int64_t pairs = in->seqs / 2;
   return by_dtype(in->dtype, [&](auto io) {
     using Io = decltype(io);
@@ -298,8 +302,36 @@ int launch_preference(const finetune_logits* in, const float* ref, const finetun
     const int st = launch_rows<Io>(in, split, logp, lse, again, ws, s);
     if (st != RDFFT_OK) return st;
     hipLaunchKernelGGL((preference_kernel<Io>), dim3(grid_of(pairs)), dim3(kLogitThreads), 0, s,
-                       join_of<Io>(in, split, lse, ws), in->labels, logp, ref, p, loss, logratio, slope, pairs,
+                       join_of<Io>(in, split, lse, ws), in->labels, logp, ref, preference_of(how), res, pairs,
                        in->positions);
+    return launch_status();
+  });
+}
+
+// Whether a step's gradient kernel works the slopes out for itself: rows enough
+// to fill the chip would each repeat what one launch does once.
+bool few_rows(const finetune_logits* in) { return logit_rows(in) > 0 && logit_rows(in) < kWantGroups; }
+// ... with `more` workgroups for what is not a row's gradient
+unsigned few_rows_grid(const finetune_logits* in, const RowSplit& split, int64_t more) {
+  return static_cast<unsigned>(more + logit_rows(in) * split.parts);
+}
+
+int launch_preference_step(const finetune_logits* in, const float* ref, const finetune_preference* how, float scale,
+                           const PreferenceOut& res, float* logp, float* lse, const finetune_dlogits* out, void* ws,
+                           hipStream_t s) {
+  if (!few_rows(in)) {
+    const int st = launch_preference(in, ref, how, res, logp, lse, true, ws, s);
+    if (st != RDFFT_OK) return st;
+    return launch_grad(in, lse, RowScale{nullptr, res.slope, scale, 1, false}, out, s);
+  }
+  return by_dtype(in->dtype, [&](auto io) {
+    using Io = decltype(io);
+    const RowSplit split = row_split(in);
+    const int st = launch_rows<Io>(in, split, logp, lse, true, ws, s);
+    if (st != RDFFT_OK) return st;
+    hipLaunchKernelGGL((preference_grad_kernel<Io>), dim3(few_rows_grid(in, split, in->seqs / 2)),
+                       dim3(kLogitThreads), 0, s, join_of<Io>(in, split, lse, ws), in->labels, logp, ref, preference_of(how), scale, res,
+                       rows_of<Io>(out), in->seqs / 2, in->positions, split.parts, split.per);
     return launch_status();
   });
 }
@@ -351,16 +383,15 @@ int launch_policy(const finetune_logits* in, const PolicyCall& c, float* stats, 
     int st = launch_rows<Io>(in, split, logp, lse, again, ws, s);
     if (st != RDFFT_OK) return st;
     if (rows <= kPolicyOne) {
-      hipLaunchKernelGGL((policy_kernel<Io, true>), dim3(1), dim3(kPolicyThreads), 0, s,
-                         join_of<Io>(in, split, lse, ws), in->labels, logp, c.in, c.weight, c.counts, c.total, c.how,
-                         stats, slope, c.terms, in->seqs, in->positions);
+      hipLaunchKernelGGL((policy_kernel<Io>), dim3(1), dim3(kPolicyThreads), 0, s, join_of<Io>(in, split, lse, ws),
+                         in->labels, logp, c.in, c.weight, c.counts, c.total, c.how, stats, slope, in->seqs,
+                         in->positions);
       return launch_status();
     }
     st = launch_policy_count(in, c, s);
     if (st != RDFFT_OK) return st;
-    hipLaunchKernelGGL((policy_kernel<Io, false>), dim3(grid_of(ceil_div(rows, kLogitThreads))), dim3(kLogitThreads),
-                       0, s, join_of<Io>(in, split, lse, ws), in->labels, logp, c.in, c.weight, c.counts, c.total,
-                       c.how, stats, slope, c.terms, in->seqs, in->positions);
+    hipLaunchKernelGGL((policy_rows_kernel), dim3(grid_of(ceil_div(rows, kLogitThreads))), dim3(kLogitThreads), 0, s,
+                       in->labels, logp, c.in, c.weight, c.how, slope, c.terms, rows, in->positions);
     st = launch_status();
     return st == RDFFT_OK ? launch_policy_sum(in, c, stats, s) : st;
   });
@@ -388,6 +419,17 @@ bool by_held_row(const finetune_logits* in, F f) {
 
 int launch_policy_step(const finetune_logits* in, const PolicyCall& c, float scale, float* stats, float* logp,
                        float* lse, float* slope, const finetune_dlogits* out, void* ws, hipStream_t s) {
+  if (few_rows(in))
+    return by_dtype(in->dtype, [&](auto io) {
+      using Io = decltype(io);
+      const RowSplit split = row_split(in);
+      const int st = launch_rows<Io>(in, split, logp, lse, true, ws, s);
+      if (st != RDFFT_OK) return st;
+      hipLaunchKernelGGL((policy_grad_kernel<Io>), dim3(few_rows_grid(in, split, 1)), dim3(kLogitThreads), 0, s,
+                         join_of<Io>(in, split, lse, ws), in->labels, logp, c.in, c.weight, c.counts, c.total, c.how,
+                         scale, stats, slope, rows_of<Io>(out), in->seqs, in->positions, split.parts, split.per);
+      return launch_status();
+    });
   const bool held = by_held_row(in, [](auto, auto) {});
   if (!held) {
     const int st = launch_policy(in, c, stats, logp, lse, slope, true, ws, s);
@@ -617,7 +659,7 @@ int preference_loss_fwd(const finetune_logits* in, const float* ref_logp, const 
   const Array outs[] = {{loss, in->seqs / 2}, {logratio, in->seqs}, {logp, rows}, {lse, rows}, {slope, in->seqs}};
   if (st == RDFFT_OK) st = check_arrays(in, nullptr, ins, outs, ws, need);
   if (st != RDFFT_OK) return st;
-  return launch_preference(in, ref_logp, how, loss, logratio, logp, lse, slope, false, ws,
+  return launch_preference(in, ref_logp, how, PreferenceOut{loss, logratio, slope}, logp, lse, false, ws,
                            static_cast<hipStream_t>(stream));
 }
 
@@ -647,10 +689,8 @@ int preference_loss_step(const finetune_logits* in, const float* ref_logp, const
   const Array outs[] = {{loss, in->seqs / 2}, {logratio, in->seqs}, {logp, rows}, {lse, rows}, {slope, in->seqs}};
   if (st == RDFFT_OK) st = check_arrays(in, out, ins, outs, ws, need);
   if (st != RDFFT_OK) return st;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  st = launch_preference(in, ref_logp, how, loss, logratio, logp, lse, slope, true, ws, s);
-  if (st != RDFFT_OK) return st;
-  return launch_grad(in, lse, RowScale{nullptr, slope, static_cast<float>(scale), 1, false}, out, s);
+  return launch_preference_step(in, ref_logp, how, static_cast<float>(scale), PreferenceOut{loss, logratio, slope},
+                                logp, lse, out, ws, static_cast<hipStream_t>(stream));
 }
 
 int policy_loss_fwd(const finetune_logits* in, const float* old_logp, const float* ref_logp, const float* advantages,

@@ -133,12 +133,13 @@ __device__ __forceinline__ MaxSum row_max_sum(const typename Io::T* x, int begin
 // lse and logp of every position.  One workgroup per row (parts = 1), or, where
 // there are fewer rows than the chip has room for, `parts` workgroups of `per`
 // columns each, whose maxima and sums go to `partial` for the next kernel to
-// join.  STREAM: rows below `keep` are read past the caches, the others through
+// join, and the label's logit to `picked`: the next kernel may replace it.
+// STREAM: rows below `keep` are read past the caches, the others through
 // them.
 template <class Io, int NT, bool STREAM>
 __global__ void __launch_bounds__(NT)
-    token_logprob_kernel(Rows<Io> in, const int64_t* labels, float* logp, float* lse, float2* partial, int64_t rows,
-                         int64_t positions, int v, int parts, int per, int64_t keep) {
+    token_logprob_kernel(Rows<Io> in, const int64_t* labels, float* logp, float* lse, float2* partial,
+                         float* picked, int64_t rows, int64_t positions, int v, int parts, int per, int64_t keep) {
   __shared__ float sm[2 * NT / kWave + 1];
   for (int64_t i = blockIdx.x; i < rows * parts; i += gridDim.x) {
     const int64_t r = parts == 1 ? i : static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(parts));
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(NT)
     if (threadIdx.x == 0) {
       if (parts > 1) {
         partial[i] = make_float2(a.m, a.s);
+        if (label >= begin && label < end) picked[r] = Io::widen(x[label]);
       } else {
         const double l = a.lse();
         lse[r] = static_cast<float>(l);
@@ -170,35 +172,51 @@ template <class Io>
 struct JoinParts {
   Rows<Io> in;
   const float2* partial;  // null: logp and lse are there already
+  const float* picked;
   float* lse;
   int parts, lanes, v;  // lanes: of one row, a power of two up to 64
 
-  // Rows [first, first + count) by the NT threads of a workgroup, `lanes` of
-  // them a row; all of its threads have the results after the barrier at the
-  // end.  (One thread a row took 8.6 us for the 64 parts of a single row.)
-  template <int NT>
-  __device__ __forceinline__ void operator()(int64_t first, int64_t count, const int64_t* labels, int64_t positions,
-                                             float* logp) const {
-    if (!partial) return;
+  // logp of row r by `lanes` threads in a row, each calling this with its index
+  // `lane` among them (r the same; label kIgnore where there is no row); lane 0
+  // has the result, and stores it and lse if `write`.  (One thread a row took
+  // 8.6 us for the 64 parts of a single row.)
+  __device__ __forceinline__ float row(int64_t r, int lane, int64_t label, float* logp, bool write,
+                                       float* lse_out = nullptr) const {
+    if (!partial) {
+      if (lse_out) *lse_out = label == kIgnore ? 0.0f : lse[r];
+      return label == kIgnore ? 0.0f : logp[r];
+    }
+    const bool known = label >= 0 && label < v;
+    MaxSum a;
+    if (known)
+      for (int k = lane; k < parts; k += lanes) {
+        const float2 q = partial[r * parts + k];
+        a.join(q.x, q.y);
+      }
+    for (int o = lanes / 2; o > 0; o /= 2) a.join(__shfl_xor(a.m, o, kWave), __shfl_xor(a.s, o, kWave));
+    if (lane != 0) return 0.0f;
+    const double l = known ? a.lse() : label == kIgnore ? 0.0 : NAN;
+    const float p = static_cast<float>(known ? picked[r] - l : l);
+    if (lse_out) *lse_out = static_cast<float>(l);
+    if (write) {
+      lse[r] = static_cast<float>(l);
+      logp[r] = p;
+    }
+    return p;
+  }
+
+  // f(row, label, logp) for rows [first, first + count), by lane 0 of each row's
+  // threads among the NT of a workgroup
+  template <int NT, class F>
+  __device__ __forceinline__ void rows(int64_t first, int64_t count, const int64_t* labels, float* logp, bool write,
+                                       F f) const {
     const int lane = static_cast<int>(threadIdx.x) & (lanes - 1), at_once = NT / lanes;
     for (int64_t base = 0; base < count; base += at_once) {
       const int64_t i = base + static_cast<int>(threadIdx.x) / lanes, r = first + i;
       const int64_t label = i < count ? labels[r] : kIgnore;
-      const bool known = label >= 0 && label < v;
-      MaxSum a;
-      if (known)
-        for (int k = lane; k < parts; k += lanes) {
-          const float2 q = partial[r * parts + k];
-          a.join(q.x, q.y);
-        }
-      for (int o = lanes / 2; o > 0; o /= 2) a.join(__shfl_xor(a.m, o, kWave), __shfl_xor(a.s, o, kWave));
-      if (lane == 0 && i < count) {
-        const double l = known ? a.lse() : label == kIgnore ? 0.0 : NAN;
-        lse[r] = static_cast<float>(l);
-        logp[r] = static_cast<float>(known ? Io::widen(in.row(r, positions)[label]) - l : l);
-      }
+      const float p = row(r, lane, label, logp, write && i < count);
+      if (lane == 0 && i < count) f(r, label, p);
     }
-    __syncthreads();
   }
 };
 
@@ -206,10 +224,10 @@ struct JoinParts {
 constexpr int kJoinRows = 64;  // of a workgroup
 template <class Io>
 __global__ void __launch_bounds__(kLogitThreads)
-    join_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, int64_t rows, int64_t positions) {
+    join_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, int64_t rows) {
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kJoinRows;
-  join.template operator()<kLogitThreads>(first, rows - first < kJoinRows ? rows - first : kJoinRows, labels,
-                                          positions, logp);
+  join.template rows<kLogitThreads>(first, rows - first < kJoinRows ? rows - first : kJoinRows, labels, logp, true,
+                                    [](int64_t, int64_t, float) {});
 }
 
 // One row's gradient g (1[j = label] - exp(x_j - lse)): with L = log2(e),
@@ -254,6 +272,35 @@ struct RowScale {
   }
 };
 
+// Columns [begin, end) of a row's gradient by NT threads; `x` and `o` are the
+// rows of the logits and of the gradient.
+template <class Io, int NT, bool STREAM>
+__device__ __forceinline__ void write_zeros(typename Io::T* o, int begin, int end) {
+  const Pieces<Io> p(o, begin, end);
+  for (int j = p.first + static_cast<int>(threadIdx.x) * Io::kVec; j < p.last; j += NT * Io::kVec)
+    store_vec<Io, STREAM>(o + j, typename Io::Vec{});
+  p.template rest<NT>([&](int c) { o[c] = 0; });
+}
+template <class Io, int NT, bool STREAM>
+__device__ __forceinline__ void write_grad(const RowGrad& grad, const typename Io::T* x, typename Io::T* o, int begin,
+                                           int end) {
+  constexpr int V = Io::kVec, U = 4;
+  const Pieces<Io> p(o, begin, end);  // aligned stores; the loads too where both rows lie alike
+  int j = p.first + static_cast<int>(threadIdx.x) * V;
+  for (; j + (U - 1) * NT * V + V <= p.last; j += U * NT * V) {
+    typename Io::Vec raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u] = load_vec<Io, STREAM>(x + j + u * NT * V);
+#pragma unroll
+    for (int u = 0; u < U; ++u) store_vec<Io, STREAM>(o + j + u * NT * V, grad.piece<Io>(raw[u], j + u * NT * V));
+  }
+  for (; j < p.last; j += NT * V) store_vec<Io, STREAM>(o + j, grad.piece<Io>(load_vec<Io, STREAM>(x + j), j));
+  p.template rest<NT>([&](int c) {
+    const float q = grad.at(Io::widen(x[c]));
+    o[c] = Io::narrow(c == grad.label ? grad.g + q : q);
+  });
+}
+
 // The gradient of every row, `parts` workgroups of `per` columns a row, the
 // last row first: a step's logits were read just before, and the last of them
 // are still in the 256 MB cache.
@@ -261,7 +308,6 @@ template <class Io, int NT, bool STREAM>
 __global__ void __launch_bounds__(NT)
     logits_grad_kernel(Rows<Io> in, const int64_t* labels, const float* lse, RowScale scale, Rows<Io> out,
                        int64_t rows, int64_t positions, int v, int parts, int per) {
-  constexpr int V = Io::kVec, U = 4;
   for (int64_t n = blockIdx.x; n < rows * parts; n += gridDim.x) {
     const int64_t i = rows * parts - 1 - n;
     const int64_t r = parts == 1 ? i : static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(parts));
@@ -269,29 +315,12 @@ __global__ void __launch_bounds__(NT)
     const int64_t label = labels[r];
     typename Io::T* o = out.row(r, positions);
     if (label == kIgnore) {
-      const Pieces<Io> p(o, begin, end);
-      for (int j = p.first + static_cast<int>(threadIdx.x) * V; j < p.last; j += NT * V)
-        store_vec<Io, STREAM>(o + j, typename Io::Vec{});
-      p.template rest<NT>([&](int c) { o[c] = 0; });
+      write_zeros<Io, NT, STREAM>(o, begin, end);
       continue;
     }
     const bool known = label >= 0 && label < v;
     const RowGrad grad(known ? scale.at(r, positions) : NAN, lse[r], known ? static_cast<int>(label) : -1);
-    const typename Io::T* x = in.row(r, positions);
-    const Pieces<Io> p(o, begin, end);  // aligned stores; the loads too where both rows lie alike
-    int j = p.first + static_cast<int>(threadIdx.x) * V;
-    for (; j + (U - 1) * NT * V + V <= p.last; j += U * NT * V) {
-      typename Io::Vec raw[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = load_vec<Io, STREAM>(x + j + u * NT * V);
-#pragma unroll
-      for (int u = 0; u < U; ++u) store_vec<Io, STREAM>(o + j + u * NT * V, grad.piece<Io>(raw[u], j + u * NT * V));
-    }
-    for (; j < p.last; j += NT * V) store_vec<Io, STREAM>(o + j, grad.piece<Io>(load_vec<Io, STREAM>(x + j), j));
-    p.template rest<NT>([&](int c) {
-      const float q = grad.at(Io::widen(x[c]));
-      o[c] = Io::narrow(c == grad.label ? grad.g + q : q);
-    });
+    write_grad<Io, NT, STREAM>(grad, in.row(r, positions), o, begin, end);
   }
 }
 
@@ -301,72 +330,126 @@ struct Preference {
   double beta, smoothing;
 };
 
-// One workgroup per pair: both sequences' log-ratios, the loss and the slopes.
+// A pair's loss, log-ratios and slopes, in every thread of a workgroup of NT.
 // The sums run in fp64 (a few values per thread), all four of them through one
-// barrier.
+// barrier; `s` may be reused after the next one.
+struct Pair {
+  double loss, ratio[2], slope[2];
+};
+template <class Io, int NT>
+__device__ __forceinline__ Pair pair_of(const JoinParts<Io>& join, const int64_t* labels, float* logp, const float* ref,
+                                        const Preference& how, int64_t b, int64_t pairs, int64_t positions, bool write,
+                                        double (&s)[4][NT / kWave]) {
+  constexpr int W = NT / kWave;
+  double sum[4] = {};  // log-ratio and count of the chosen sequence, then of the rejected one
+#pragma unroll
+  for (int side = 0; side < 2; ++side)
+    join.template rows<NT>((b + side * pairs) * positions, positions, labels, logp, write,
+                           [&](int64_t r, int64_t label, float p) {
+                             if (label == kIgnore) return;
+                             sum[2 * side] += static_cast<double>(p) - static_cast<double>(ref[r]);
+                             sum[2 * side + 1] += 1.0;
+                           });
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    sum[k] = lanes_sum<kWave>(sum[k]);
+    if (threadIdx.x % kWave == 0) s[k][threadIdx.x / kWave] = sum[k];
+  }
+  __syncthreads();
+  Pair q;
+  double count[2];
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    double a = 0.0, c = 0.0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      a += s[2 * side][w];
+      c += s[2 * side + 1][w];
+    }
+    count[side] = how.average && c > 0.0 ? c : 1.0;
+    q.ratio[side] = a / count[side];
+  }
+  const double h = q.ratio[0] - q.ratio[1], z = how.beta * h, e = how.smoothing;
+  double dh;
+  if (how.kind == 0) {
+    const double t = exp(-fabs(z)), up = (z < 0.0 ? z : 0.0) - log1p(t);  // log sigma(z); log sigma(-z) = up - z
+    const double big = 1.0 / (1.0 + t), small = t * big;                  // sigma(|z|) and sigma(-|z|)
+    q.loss = -(1.0 - e) * up - e * (up - z);
+    dh = z < 0.0 ? -how.beta * ((1.0 - e) * big - e * small) : -how.beta * ((1.0 - e) * small - e * big);
+  } else if (how.kind == 1) {
+    q.loss = z < 1.0 ? 1.0 - z : z >= 1.0 ? 0.0 : z;  // the last: NaN
+    dh = z < 1.0 ? -how.beta : z >= 1.0 ? 0.0 : z;
+  } else {
+    const double gap = h - 0.5 / how.beta;
+    q.loss = gap * gap;
+    dh = 2.0 * gap;
+  }
+  q.slope[0] = dh / count[0];
+  q.slope[1] = -dh / count[1];
+  return q;
+}
+
+struct PreferenceOut {
+  float *loss, *logratio, *slope;
+  __device__ __forceinline__ void store(const Pair& q, int64_t b, int64_t pairs) const {
+    if (threadIdx.x != 0) return;
+    loss[b] = static_cast<float>(q.loss);
+    logratio[b] = static_cast<float>(q.ratio[0]);
+    logratio[b + pairs] = static_cast<float>(q.ratio[1]);
+    slope[b] = static_cast<float>(q.slope[0]);
+    slope[b + pairs] = static_cast<float>(q.slope[1]);
+  }
+};
+
 template <class Io>
 __global__ void __launch_bounds__(kLogitThreads)
     preference_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, const float* ref, Preference how,
-                      float* loss, float* logratio, float* slope, int64_t pairs, int64_t positions) {
-  constexpr int W = kLogitThreads / kWave;
-  __shared__ double s[4][W];
+                      PreferenceOut out, int64_t pairs, int64_t positions) {
+  __shared__ double s[4][kLogitThreads / kWave];
   for (int64_t b = blockIdx.x; b < pairs; b += gridDim.x) {
-    for (int side = 0; side < 2; ++side)
-      join.template operator()<kLogitThreads>((b + side * pairs) * positions, positions, labels, positions, logp);
-    double sum[4] = {};  // log-ratio and count of the chosen sequence, then of the rejected one
-    for (int64_t i = threadIdx.x; i < positions; i += kLogitThreads) {
-#pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        const int64_t r = (b + side * pairs) * positions + i, label = labels[r];
-        const double p = logp[r], q = ref[r];
-        if (label != kIgnore) {
-          sum[2 * side] += p - q;
-          sum[2 * side + 1] += 1.0;
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      sum[k] = lanes_sum<kWave>(sum[k]);
-      if (threadIdx.x % kWave == 0) s[k][threadIdx.x / kWave] = sum[k];
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      double ratio[2], count[2];
-#pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        double a = 0.0, c = 0.0;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          a += s[2 * side][w];
-          c += s[2 * side + 1][w];
-        }
-        count[side] = how.average && c > 0.0 ? c : 1.0;
-        ratio[side] = a / count[side];
-      }
-      const double h = ratio[0] - ratio[1], z = how.beta * h, e = how.smoothing;
-      double l, dh;
-      if (how.kind == 0) {
-        const double t = exp(-fabs(z)), up = (z < 0.0 ? z : 0.0) - log1p(t);  // log sigma(z); log sigma(-z) = up - z
-        const double big = 1.0 / (1.0 + t), small = t * big;                  // sigma(|z|) and sigma(-|z|)
-        l = -(1.0 - e) * up - e * (up - z);
-        dh = z < 0.0 ? -how.beta * ((1.0 - e) * big - e * small) : -how.beta * ((1.0 - e) * small - e * big);
-      } else if (how.kind == 1) {
-        l = z < 1.0 ? 1.0 - z : z >= 1.0 ? 0.0 : z;  // the last: NaN
-        dh = z < 1.0 ? -how.beta : z >= 1.0 ? 0.0 : z;
-      } else {
-        const double gap = h - 0.5 / how.beta;
-        l = gap * gap;
-        dh = 2.0 * gap;
-      }
-      loss[b] = static_cast<float>(l);
-      logratio[b] = static_cast<float>(ratio[0]);
-      logratio[b + pairs] = static_cast<float>(ratio[1]);
-      slope[b] = static_cast<float>(dh / count[0]);
-      slope[b + pairs] = static_cast<float>(-dh / count[1]);
-    }
+    out.store(pair_of<Io, kLogitThreads>(join, labels, logp, ref, how, b, pairs, positions, true, s), b, pairs);
     __syncthreads();
   }
+}
+
+// The step's second and last launch where there are few rows: every workgroup
+// works its pair's slope out for itself and writes its part of a row's
+// gradient, and one more a pair writes the pair's results.  A launch more costs the
+// host 5 us (a pair of 16 x 1009 fp32: 14.4 us with it, 10.5 us so).
+template <class Io>
+__global__ void __launch_bounds__(kLogitThreads)
+    preference_grad_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, const float* ref, Preference how,
+                           float scale, PreferenceOut res, Rows<Io> out, int64_t pairs, int64_t positions, int parts,
+                           int per) {
+  constexpr int NT = kLogitThreads;
+  __shared__ double s[4][NT / kWave];
+  __shared__ float told;
+  if (blockIdx.x < pairs) {
+    res.store(pair_of<Io, NT>(join, labels, logp, ref, how, blockIdx.x, pairs, positions, true, s), blockIdx.x, pairs);
+    return;
+  }
+  const uint32_t i = blockIdx.x - static_cast<uint32_t>(pairs), r = i / static_cast<uint32_t>(parts);
+  const int begin = static_cast<int>(i - r * parts) * per, end = begin + per < join.v ? begin + per : join.v;
+  const int64_t label = labels[r];
+  typename Io::T* o = out.row(r, positions);
+  if (label == kIgnore) {
+    write_zeros<Io, NT, false>(o, begin, end);
+    return;
+  }
+  const uint32_t seq = r / static_cast<uint32_t>(positions);
+  const bool chosen = seq < pairs;
+  const Pair q = pair_of<Io, NT>(join, labels, logp, ref, how, chosen ? seq : seq - pairs, pairs, positions, false, s);
+  float lse = 0.0f;
+  const int lane = static_cast<int>(threadIdx.x);
+  if (lane < kWave) {  // one wave: this row's lse from its parts
+    join.row(r, lane < join.lanes ? lane : join.parts, label, logp, false, &lse);
+    if (lane == 0) told = lse;
+  }
+  __syncthreads();
+  const bool known = label >= 0 && label < join.v;
+  const float slope = static_cast<float>(chosen ? q.slope[0] : q.slope[1]);
+  const RowGrad grad(known ? scale * slope : NAN, told, known ? static_cast<int>(label) : -1);
+  write_grad<Io, NT, false>(grad, join.in.row(r, positions), o, begin, end);
 }
 
 struct Policy {
@@ -416,19 +499,20 @@ struct PolicyInputs {
 
 constexpr int kPolicyThreads = 1024;
 
-// The counts that the reduction needs, by one workgroup: all positions at once,
-// or a wave for a sequence at a time.
+// The counts that the reduction needs, by one workgroup of NT: all positions at
+// once, or a wave for a sequence at a time.
+template <int NT>
 __device__ __forceinline__ void policy_counts(const int64_t* labels, int* counts, int* total, int reduction,
                                               int64_t seqs, int64_t positions, int* s) {
   if (reduction == 0) {
     int c = 0;
 #pragma unroll 8
-    for (int64_t r = threadIdx.x; r < seqs * positions; r += kPolicyThreads) c += labels[r] != kIgnore;
-    c = block_sum<kPolicyThreads>(c, s);
+    for (int64_t r = threadIdx.x; r < seqs * positions; r += NT) c += labels[r] != kIgnore;
+    c = block_sum<NT>(c, s);
     if (threadIdx.x == 0) total[0] = c;
   } else if (reduction == 1) {
     const int lane = threadIdx.x % kWave;
-    for (int64_t q = threadIdx.x / kWave; q < seqs; q += kPolicyThreads / kWave) {
+    for (int64_t q = threadIdx.x / kWave; q < seqs; q += NT / kWave) {
       int c = 0;
 #pragma unroll 8
       for (int64_t i = lane; i < positions; i += kWave) c += labels[q * positions + i] != kIgnore;
@@ -442,55 +526,118 @@ __global__ void __launch_bounds__(kPolicyThreads)
     policy_count_kernel(const int64_t* labels, int* counts, int* total, int reduction, int64_t seqs,
                         int64_t positions) {
   __shared__ int s[kPolicyThreads / kWave];
-  policy_counts(labels, counts, total, reduction, seqs, positions, s);
+  policy_counts<kPolicyThreads>(labels, counts, total, reduction, seqs, positions, s);
 }
 
-// Every position's slope, and the reduced loss and KL.  ONE: everything in one
-// workgroup, the counts too; else a thread a row, whose shares go to `terms`
-// for policy_sum_kernel, after policy_count_kernel.
-template <class Io, bool ONE>
-__global__ void __launch_bounds__(ONE ? kPolicyThreads : kLogitThreads)
+// A position's slope and its shares of the loss and the KL.
+struct PolicyShare {
+  float slope = 0.0f;
+  double2 share = make_double2(0.0, 0.0);
+};
+__device__ __forceinline__ PolicyShare policy_share(const Policy& how, const PolicyInputs& in, double weight, int64_t r,
+                                                    int64_t seq, float logp) {
+  const PolicyTerm e = policy_term(how, logp, in.old[r], in.ref != nullptr, in.ref ? in.ref[r] : 0.0f,
+                                   in.adv[in.per_token ? r : seq]);
+  return {static_cast<float>(weight * e.slope), make_double2(weight * e.loss, weight * e.kl)};
+}
+
+// Every position's logp, lse and slope, and the reduced loss and KL, by one
+// workgroup of NT.
+template <class Io, int NT>
+__device__ __forceinline__ void policy_all(const JoinParts<Io>& join, const int64_t* labels, float* logp,
+                                           const PolicyInputs& in, const PolicyWeight& weight, int* counts, int* total,
+                                           const Policy& how, float* stats, float* slope, int64_t seqs,
+                                           int64_t positions, int (&sc)[NT / kWave], double (&s)[2][NT / kWave]) {
+  policy_counts<NT>(labels, counts, total, how.reduction, seqs, positions, sc);
+  __syncthreads();
+  const uint32_t n = static_cast<uint32_t>(positions);
+  double a = 0.0, k = 0.0;
+  join.template rows<NT>(0, seqs * positions, labels, logp, true, [&](int64_t r, int64_t label, float p) {
+    PolicyShare e;
+    const uint32_t seq = static_cast<uint32_t>(r) / n;
+    if (label != kIgnore) e = policy_share(how, in, weight.of(weight.count(seq)), r, seq, p);
+    slope[r] = e.slope;
+    a += e.share.x;
+    k += e.share.y;
+  });
+  a = block_sum<NT>(a, s[0]);
+  k = block_sum<NT>(k, s[1]);
+  if (threadIdx.x == 0) {
+    stats[0] = static_cast<float>(a);
+    stats[1] = static_cast<float>(k);
+  }
+}
+
+template <class Io>
+__global__ void __launch_bounds__(kPolicyThreads)
     policy_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, PolicyInputs in, PolicyWeight weight,
-                  int* counts, int* total, Policy how, float* stats, float* slope, double2* terms, int64_t seqs,
-                  int64_t positions) {
-  constexpr int NT = ONE ? kPolicyThreads : kLogitThreads;
+                  int* counts, int* total, Policy how, float* stats, float* slope, int64_t seqs, int64_t positions) {
+  __shared__ double s[2][kPolicyThreads / kWave];
+  __shared__ int sc[kPolicyThreads / kWave];
+  policy_all<Io, kPolicyThreads>(join, labels, logp, in, weight, counts, total, how, stats, slope, seqs, positions, sc,
+                                 s);
+}
+
+// The same for many rows, none of them in parts: a thread a row, whose shares go
+// to `terms` for policy_sum_kernel, after policy_count_kernel.
+__global__ void __launch_bounds__(kLogitThreads)
+    policy_rows_kernel(const int64_t* labels, const float* logp, PolicyInputs in, PolicyWeight weight, Policy how,
+                       float* slope, double2* terms, int64_t rows, int64_t positions) {
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kLogitThreads + threadIdx.x; r < rows;
+       r += static_cast<int64_t>(gridDim.x) * kLogitThreads) {
+    PolicyShare e;
+    const uint32_t seq = static_cast<uint32_t>(r) / static_cast<uint32_t>(positions);
+    if (labels[r] != kIgnore) e = policy_share(how, in, weight.of(weight.count(seq)), r, seq, logp[r]);
+    slope[r] = e.slope;
+    terms[r] = e.share;
+  }
+}
+
+// The step's second and last launch where there are few rows: every workgroup
+// works its row's slope out for itself and writes its part of the gradient, the
+// first one everything else (4 x 8 x 32768 half: 14.6 us with a launch between,
+// 10.8 us so).
+template <class Io>
+__global__ void __launch_bounds__(kLogitThreads)
+    policy_grad_kernel(JoinParts<Io> join, const int64_t* labels, float* logp, PolicyInputs in, PolicyWeight weight,
+                       int* counts, int* total, Policy how, float scale, float* stats, float* slope, Rows<Io> out,
+                       int64_t seqs, int64_t positions, int parts, int per) {
+  constexpr int NT = kLogitThreads;
   __shared__ double s[2][NT / kWave];
   __shared__ int sc[NT / kWave];
-  if constexpr (ONE) {
-    policy_counts(labels, counts, total, how.reduction, seqs, positions, sc);
-    join.template operator()<NT>(0, seqs * positions, labels, positions, logp);
-    __syncthreads();
+  __shared__ float told[2];
+  if (blockIdx.x == 0) {
+    policy_all<Io, NT>(join, labels, logp, in, weight, counts, total, how, stats, slope, seqs, positions, sc, s);
+    return;
   }
-  const uint32_t rows = static_cast<uint32_t>(seqs * positions), n = static_cast<uint32_t>(positions);
-  double a = 0.0, k = 0.0;
-  for (uint32_t r = blockIdx.x * NT + threadIdx.x; r < rows; r += gridDim.x * NT) {
-    const int64_t label = labels[r];
-    const float p = logp[r];  // (rows in parts are few: they come with ONE)
-    double2 t = make_double2(0.0, 0.0);
-    float g = 0.0f;
-    if (label != kIgnore) {
-      const double w = weight.of(weight.count(r / n));
-      const PolicyTerm e = policy_term(how, p, in.old[r], in.ref != nullptr, in.ref ? in.ref[r] : 0.0f,
-                                       in.adv[in.per_token ? r : r / n]);
-      t = make_double2(w * e.loss, w * e.kl);
-      g = static_cast<float>(w * e.slope);
-    }
-    slope[r] = g;
-    if (ONE) {
-      a += t.x;
-      k += t.y;
-    } else {
-      terms[r] = t;
-    }
+  const uint32_t i = blockIdx.x - 1, r = i / static_cast<uint32_t>(parts), n = static_cast<uint32_t>(positions);
+  const int begin = static_cast<int>(i - r * parts) * per, end = begin + per < join.v ? begin + per : join.v;
+  const int64_t label = labels[r];
+  typename Io::T* o = out.row(r, positions);
+  if (label == kIgnore) {
+    write_zeros<Io, NT, false>(o, begin, end);
+    return;
   }
-  if constexpr (ONE) {
-    a = block_sum<NT>(a, s[0]);
-    k = block_sum<NT>(k, s[1]);
-    if (threadIdx.x == 0) {
-      stats[0] = static_cast<float>(a);
-      stats[1] = static_cast<float>(k);
+  const uint32_t seq = r / n;
+  int c = 0;
+  if (how.reduction != 2) {
+    const int64_t first = how.reduction == 0 ? 0 : static_cast<int64_t>(seq) * n, last = how.reduction == 0 ? seqs * n : first + n;
+    for (int64_t k = first + threadIdx.x; k < last; k += NT) c += labels[k] != kIgnore;
+    c = block_sum<NT>(c, sc);
+  }
+  const int lane = static_cast<int>(threadIdx.x);
+  if (lane < kWave) {  // one wave: this row from its parts
+    float lse = 0.0f;
+    const float p = join.row(r, lane < join.lanes ? lane : join.parts, label, logp, false, &lse);
+    if (lane == 0) {
+      told[0] = lse;
+      told[1] = scale * policy_share(how, in, weight.of(how.reduction == 2 ? 1 : c), r, seq, p).slope;
     }
   }
+  __syncthreads();
+  const bool known = label >= 0 && label < join.v;
+  const RowGrad grad(known ? told[1] : NAN, told[0], known ? static_cast<int>(label) : -1);
+  write_grad<Io, NT, false>(grad, join.in.row(r, positions), o, begin, end);
 }
 
 // The positions' shares summed in a fixed order.

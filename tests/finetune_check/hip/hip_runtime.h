@@ -168,6 +168,9 @@ inline void __syncthreads() { pthread_barrier_wait(emu::ctx.group); }
 #define __builtin_amdgcn_permlane32_swap(a, b, x, y) emu::swap_runs(a, b, 32)
 #define __builtin_amdgcn_exp2f(x) std::exp2(x)
 
+inline float __shfl_xor(float v, int mask, int) {
+  return __builtin_bit_cast(float, emu::lane_read(__builtin_bit_cast(uint32_t, v), [mask](unsigned l) { return l ^ mask; }));
+}
 inline float __uint_as_float(uint32_t u) { return __builtin_bit_cast(float, u); }
 
 #define hipLaunchKernelGGL(kernel, grid, block, lds, stream, ...) \

@@ -44,6 +44,11 @@ def store_err(want, dtype):
     return s * np.abs(want) * 1.01 + tiny
 
 
+def representable(want, dtype):
+    """want with what rounds past the storage type's largest value as infinity (half: from 65520 on)."""
+    return np.where(np.abs(want) >= 65520.0, np.copysign(np.inf, want), want) if dtype == "f16" else want
+
+
 def within(got, want, bound):
     """Every element of got within bound of want (equal NaN and infinity included)."""
     got, want, bound = np.asarray(got, float), np.asarray(want, float), np.asarray(bound, float)

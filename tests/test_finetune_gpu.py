@@ -720,3 +720,36 @@ def test_policy_step_many_rows(v, dtype):
     first = bcl.policy_loss_step(xd, dev(lab, torch.int64), full_old.view(n, t), full_adv.view(n, t))[1]
     bcl.policy_loss_step(xd, dev(lab, torch.int64), full_old.view(n, t), full_adv.view(n, t), dlogits=xd)
     assert torch.equal(xd, first)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,t,v", [(2, 1, 131073), (2, 3, 70001), (4, 60, 9000), (6, 5, 300), (200, 2, 130), (2, 400, 517),
+                                   (2, 255, 4099), (2, 256, 4099)])
+def test_steps_in_place_equal_steps_apart(n, t, v, dtype):
+    # the gradient over the logits themselves: rows in parts, whole rows, either side of the row count that
+    # changes the kernels; equal to the gradient beside them and, up to rounding, to the separate calls
+    xt, x, lab = fu.logit_case((70, n, t, v), n, t, v, dtype, masked=0.3, empty=(1,) if n > 2 else ())
+    xd, ld = xt.to(DEV), dev(lab, torch.int64)
+    r0 = rng(71, n, t)
+    ref = dev(r0.standard_normal((n, t)) - np.log(v))
+    adv = dev(r0.standard_normal(n))
+    logp0, lse0 = fo.token_logprob(x, lab)
+    for kind in ("sigmoid", "ipo"):
+        a, d = bcl.preference_loss_step(xd, ld, ref, kind=kind, average=True)
+        buf = xd.clone()
+        b, e = bcl.preference_loss_step(buf, ld, ref, kind=kind, average=True, dlogits=buf)
+        assert e is buf and torch.equal(d, buf) and all(torch.equal(p, q) for p, q in zip(a, b))
+        f = bcl.preference_loss_fwd(xd, ld, ref, kind=kind, average=True)
+        assert all(torch.equal(p, q) for p, q in zip(a, f))
+    for reduction in ("token", "sequence", "sum"):
+        kw = dict(ref_logp=ref, kl_coef=0.1, reduction=reduction)
+        a, d = bcl.policy_loss_step(xd, ld, ref, adv, **kw)
+        buf = xd.clone()
+        b, e = bcl.policy_loss_step(buf, ld, ref, adv, dlogits=buf, **kw)
+        assert e is buf and torch.equal(d, buf) and all(torch.equal(p, q) for p, q in zip(a, b))
+        check_logp(x, lab, a.logp, a.lse, lse0, logp0)
+        f = bcl.policy_loss_fwd(xd, ld, ref, adv, **kw)
+        for p, q in zip(a, f):
+            within(f64(p), f64(q), 1e-5 * (1 + np.abs(f64(q))))
+        want = fo.logits_grad(x, lab, f64(a.slope))
+        within(f64(d), fu.representable(want, dtype), fu.grad_err(want, x, lab, f64(a.slope), lse0, dtype) * 1.5)
