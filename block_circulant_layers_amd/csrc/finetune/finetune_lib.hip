@@ -301,7 +301,7 @@ int launch_preference(const finetune_logits* in, const float* ref, const finetun
     const RowSplit split = row_split(in);
     const int st = launch_rows<Io>(in, split, logp, lse, again, ws, s);
     if (st != RDFFT_OK) return st;
-    hipLaunchKernelGGL((preference_kernel<Io>), dim3(grid_of(pairs)), dim3(kLogitThreads), 0, s,
+    hipLaunchKernelGGL((preference_kernel<Io>), dim3(grid_of(pairs)), dim3(kPairThreads), 0, s,
                        join_of<Io>(in, split, lse, ws), in->labels, logp, ref, preference_of(how), res, pairs,
                        in->positions);
     return launch_status();
