@@ -46,7 +46,7 @@ unsigned grid_of(int64_t n) { return static_cast<unsigned>(n < kMaxGrid ? n : kM
 
 // threads that hold a row of d elements, 0 for the kernels of any length
 int norm_threads(int64_t d) {
-  for (int t : {8, 64, 256, 1024})
+  for (int t = 8; t <= 1024; t *= 2)
     if (d <= t * kNormElems) return t;
   return 0;
 }
@@ -62,8 +62,12 @@ void by_norm_row(int64_t d, F f) {
   };
   switch (norm_threads(d)) {
     case 8: ragged(std::integral_constant<int, 8>{}); break;
+    case 16: ragged(std::integral_constant<int, 16>{}); break;
+    case 32: ragged(std::integral_constant<int, 32>{}); break;
     case 64: ragged(std::integral_constant<int, 64>{}); break;
+    case 128: ragged(std::integral_constant<int, 128>{}); break;
     case 256: ragged(std::integral_constant<int, 256>{}); break;
+    case 512: ragged(std::integral_constant<int, 512>{}); break;
     default: ragged(std::integral_constant<int, 1024>{}); break;
   }
 }
@@ -104,7 +108,7 @@ int launch_norm_fwd(const void* x, const float* w, const float* b, void* y, floa
   by_norm_row<Io>(d, [&](auto t, auto ragged) {
     constexpr int TT = decltype(t)::value, WG = norm_wg(TT);
     const int64_t groups = ceil_div(rows, WG / TT);
-    const int64_t grid = std::min<int64_t>(groups, TT == 1024 ? 512 : 2048);
+    const int64_t grid = std::min<int64_t>(groups, 2048 * kNormThreads / WG);
     by_stream(past_caches(2 * rows * d * int64_t(sizeof(T))), [&](auto stream) {
       hipLaunchKernelGGL((layer_norm_fwd_kernel<Io, TT, decltype(ragged)::value, decltype(stream)::value>),
                          dim3(static_cast<unsigned>(grid)), dim3(WG), 0, s, px, w, b, py, mean, rstd, rows, n, xs, ys,

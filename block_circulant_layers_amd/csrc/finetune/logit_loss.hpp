@@ -340,14 +340,28 @@ __device__ __forceinline__ Pair pair_of(const JoinParts<Io>& join, const int64_t
                                         double (&s)[4][NT / kWave]) {
   constexpr int W = NT / kWave;
   double sum[4] = {};  // log-ratio and count of the chosen sequence, then of the rejected one
+  if (!join.partial) {
+    // all loads of a round at once, masked positions' too
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < positions; i += NT) {
 #pragma unroll
-  for (int side = 0; side < 2; ++side)
-    join.template rows<NT>((b + side * pairs) * positions, positions, labels, logp, write,
-                           [&](int64_t r, int64_t label, float p) {
-                             if (label == kIgnore) return;
-                             sum[2 * side] += static_cast<double>(p) - static_cast<double>(ref[r]);
-                             sum[2 * side + 1] += 1.0;
-                           });
+      for (int side = 0; side < 2; ++side) {
+        const int64_t r = (b + side * pairs) * positions + i, label = labels[r];
+        const double p = logp[r], q = ref[r];
+        sum[2 * side] += label == kIgnore ? 0.0 : p - q;
+        sum[2 * side + 1] += label == kIgnore ? 0.0 : 1.0;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+      join.template rows<NT>((b + side * pairs) * positions, positions, labels, logp, write,
+                             [&](int64_t r, int64_t label, float p) {
+                               if (label == kIgnore) return;
+                               sum[2 * side] += static_cast<double>(p) - static_cast<double>(ref[r]);
+                               sum[2 * side + 1] += 1.0;
+                             });
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     sum[k] = lanes_sum<kWave>(sum[k]);
