@@ -163,7 +163,12 @@ Rows<Io> rows_of(const finetune_dlogits* out) {
 
 // How a launch over rows of `vocab` columns is split: `nt` threads a
 // workgroup, `parts` workgroups of `per` columns a row.  A row of up to four
-// pieces a lane takes one wave.  Fewer rows than kWantGroups workgroups, two a
+// pieces a lane takes one wave, of up to 16 where kManyRows fill the chip with
+// waves: no barrier, and one reduction of lanes.  (One wave a row / a workgroup a
+// row, bf16, a forward and a step: 16384 rows of 2000, 24 / 35 us and 43 / 61 us;
+// of 8000, 45 / 56 and 104 / 112; 4096 of 8000, 19.4 / 19.9 and 38.8 / 37.9; 1024
+// of 8000, 13.1 / 12.5 and 22.0 / 20.7.  16384 rows of 16000: 65 / 72 and 199 /
+// 197.)  Fewer rows than kWantGroups workgroups, two a
 // compute unit, are split until there are as many, or until a part holds one
 // piece a thread.  (With 1024 as the limit, 999 rows of 10007 fp32 took 15.1 us
 // in two parts each and their joins, 13.4 us whole; a step of 512 rows of 50001
@@ -173,13 +178,14 @@ Rows<Io> rows_of(const finetune_dlogits* out) {
 #define FINETUNE_WANT_GROUPS 512
 #endif
 constexpr int64_t kWantGroups = FINETUNE_WANT_GROUPS;
+constexpr int64_t kManyRows = 8 * kWantGroups;
 struct RowSplit {
   int nt, parts, per;
 };
 RowSplit row_split(const finetune_logits* in) {
   const int64_t v = in->vocab, piece = in->dtype == RDFFT_F32 ? 4 : 8;
-  RowSplit s{v <= 4 * kWave * piece ? kWave : kLogitThreads, 1, static_cast<int>(v)};
-  const int64_t rows = logit_rows(in);
+  const int64_t rows = logit_rows(in), lane = rows < kManyRows ? 4 : 16;  // pieces a lane of a row's one wave
+  RowSplit s{v <= lane * kWave * piece ? kWave : kLogitThreads, 1, static_cast<int>(v)};
   if (rows > 0 && rows < kWantGroups && s.nt == kLogitThreads) {
     const int64_t unit = s.nt * piece;
     const int64_t parts = std::min<int64_t>(ceil_div(kWantGroups, rows), ceil_div(v, unit));

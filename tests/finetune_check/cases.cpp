@@ -346,6 +346,7 @@ int main(int argc, char** argv) {
     layer_norm_case(2, 16383, dt, 0, 1, true);
     layer_norm_case(18, 16400, dt, 3, 1, true);  // the kernels of any length
     loss_case(2, 1, 9001, dt, 0, 3, true, false);
+    loss_case(2, 32, 2100, dt, 1, 1, false, false);  // a wave a row of more pieces
     loss_case(2, 4, 4300, dt, 1, 1, true, false);    // rows held by 256 threads
     loss_case(2, 4, 20011, dt, 1, 1, false, false);  // ... by 512 and 1024
     loss_case(2, 4, 66000, dt, 0, 1, false, false);  // ... and past the widest in fp32

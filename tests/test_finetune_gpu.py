@@ -753,3 +753,24 @@ def test_steps_in_place_equal_steps_apart(n, t, v, dtype):
             within(f64(p), f64(q), 1e-5 * (1 + np.abs(f64(q))))
         want = fo.logits_grad(x, lab, f64(a.slope))
         within(f64(d), fu.representable(want, dtype), fu.grad_err(want, x, lab, f64(a.slope), lse0, dtype) * 1.5)
+
+
+@pytest.mark.parametrize("dtype,v", [("f32", 2051), ("f16", 4099), ("bf16", 8192), ("bf16", 8199)])
+@pytest.mark.parametrize("t", [2047, 2048])
+def test_many_rows_either_side_of_a_wave_a_row(t, v, dtype):
+    # rows enough that one wave takes a row of up to 16 pieces a lane, and one row a sequence fewer
+    n = 2
+    xt, x, lab = fu.logit_case((80, t, v), n, t, v, dtype, masked=0.9)
+    xd, ld = xt.to(DEV), dev(lab, torch.int64)
+    logp0, lse0 = fo.token_logprob(x, lab)
+    logp, lse = bcl.token_logprob(xd, ld)
+    check_logp(x, lab, logp, lse, lse0, logp0)
+    ref = dev(np.where(lab != IGNORE, logp0 + 0.1, 0.0))
+    r, d = bcl.preference_loss_step(xd, ld, ref, kind="ipo", average=True)
+    assert torch.equal(r.logp, logp) and torch.equal(r.lse, lse)
+    g = np.broadcast_to(f64(r.slope)[:, None], lab.shape)
+    want = fo.logits_grad(x, lab, g)
+    within(f64(d), fu.representable(want, dtype), fu.grad_err(want, x, lab, g, lse0, dtype) * 1.5)
+    buf = xd.clone()
+    bcl.preference_loss_step(buf, ld, ref, kind="ipo", average=True, dlogits=buf)
+    assert torch.equal(buf, d)
