@@ -27,9 +27,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Whether a call's large buffers of `bytes` in all go past the caches: where the
 // 256 MB cache cannot hold them until they are used again.  Both sides, layer
-// norm of rows of 4096 bf16: forward of 16384 rows (268 MB) 51 us past the
-// caches, 47 through them, of 32768 rows 101 and 107; backward of 8192 rows
-// (201 MB) 51 and 47, of 16384 rows (403 MB) 82 and 85.
+// norm of rows of 4096 bf16: forward of 16384 rows (268 MB) 52 us past the
+// caches, 48 through them, of 32768 rows 101 and 107; backward of 8192 rows
+// (201 MB) 43 and 43, of 16384 rows (403 MB) 76 and 79.
 constexpr bool past_caches(int64_t bytes) { return bytes > int64_t(320) << 20; }
 template <class F>
 void by_stream(bool stream, F f) {
