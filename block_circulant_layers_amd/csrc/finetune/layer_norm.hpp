@@ -22,7 +22,13 @@ constexpr int kNormThreads = 256;
 constexpr int kNormElems = 16;
 constexpr int norm_wg(int t) { return t > kNormThreads ? t : kNormThreads; }
 
-// RAGGED: the row's length is no multiple of a piece, so a piece may be cut.
+// RAGGED: the row's length is no multiple of a piece, so a piece may be cut.  A
+// cut piece is loaded as the row's last whole one, and settle() moves its
+// elements into place once they are wanted: with loads by element in a branch
+// of the lane that holds the cut piece, its wave waited for all of its loads at
+// once, the next row's among them (48547 rows of 1212 fp16: forward 87 us,
+// backward 192 us; of 1208 47 and 77; with whole loads 1212 take 52 and 85 us).
+// Its stores go by halves, quarters, ... of a piece.
 template <class Io, int T, bool RAGGED, bool STREAM>
 struct NormRow {
   static constexpr int V = Io::kVec;
@@ -36,17 +42,43 @@ struct NormRow {
     return RAGGED ? col(i) + e < d : col(i) < d;
   }
   __device__ __forceinline__ void load(const typename Io::T* p, int d) {
+    if (RAGGED && T == 8 && d < V) {  // no whole piece in the row
+      raw[0] = {};
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (col(0) + e < d) raw[0][e] = p[col(0) + e];
+#pragma unroll
+      for (int i = 1; i < N; ++i) raw[i] = {};
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = col(i);
       raw[i] = {};
-      if (c + V <= d) {
-        raw[i] = load_vec<Io, STREAM>(p + c);
-      } else if (RAGGED && c < d) {
+      if (c < d) raw[i] = load_vec<Io, STREAM>(p + (RAGGED && c + V > d ? d - V : c));
+    }
+  }
+  // the 32-bit words of a piece, its first `n` elements gone and zeros behind the others
+  static constexpr int W = V / 4;  // elements a word
+  typedef uint32_t Words __attribute__((ext_vector_type(4)));
+  typedef uint32_t Two __attribute__((ext_vector_type(2), aligned(2), may_alias));
+  typedef uint32_t One __attribute__((aligned(2), may_alias));
+  static __device__ __forceinline__ Words shifted(Words q, int n) {
+    if (n & (2 * W)) q = Words{q[2], q[3], 0, 0};
+    if (n & W) q = Words{q[1], q[2], q[3], 0};
+    if (W > 1 && (n & 1)) {
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (c + e < d) raw[i][e] = p[c + e];
-      }
+      for (int k = 0; k < 4; ++k) q[k] = q[k] >> 16 | (k < 3 ? q[(k + 1) % 4] << 16 : 0);
+    }
+    return q;
+  }
+  __device__ __forceinline__ void settle(int d) {
+    if (!RAGGED || (T == 8 && d < V)) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = col(i);
+      if (c < d && c + V > d)
+        raw[i] = __builtin_bit_cast(typename Io::Vec, shifted(__builtin_bit_cast(Words, raw[i]), c + V - d));
     }
   }
   __device__ __forceinline__ float at(int k) const { return Io::widen(raw[k / V][k % V]); }
@@ -60,9 +92,19 @@ struct NormRow {
       if (c + V <= d) {
         store_vec<Io, STREAM>(p + c, o);
       } else if (RAGGED && c < d) {
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (c + e < d) p[c + e] = o[e];
+        Words q = __builtin_bit_cast(Words, o);
+        typename Io::T* at = p + c;
+        if ((d - c) & (2 * W)) {
+          *reinterpret_cast<Two*>(at) = Two{q[0], q[1]};
+          q = shifted(q, 2 * W);
+          at += 2 * W;
+        }
+        if ((d - c) & W) {
+          *reinterpret_cast<One*>(at) = q[0];
+          q = shifted(q, W);
+          at += W;
+        }
+        if (W > 1 && ((d - c) & 1)) *at = static_cast<typename Io::T>(q[0]);
       }
     }
   }
@@ -108,7 +150,8 @@ __global__ void __launch_bounds__(norm_wg(T))
   if (r < rows) next.load(x + r * xs, d);
   // every thread of the workgroup makes the same number of rounds (barriers inside)
   for (int64_t r0 = first; r0 < rows; r0 += step, r += step) {
-    const Row cur = next;
+    Row cur = next;
+    cur.settle(d);
     if (r + step < rows) next.load(x + (r + step) * xs, d);
     float v[E], a = 0.0f;
 #pragma unroll
@@ -172,7 +215,9 @@ __global__ void __launch_bounds__(norm_wg(T))
   int turn = 0;
   for (int64_t r0 = first; r0 < rows; r0 += step, r += step, turn ^= 1) {
     if (!AHEAD) fetch(r);  // one row a workgroup: r = r0
-    const Row cx = nx, cg = ng;
+    Row cx = nx, cg = ng;
+    cx.settle(d);
+    cg.settle(d);
     const float mu = nm, rs = nr;
     if (AHEAD && r + step < rows) fetch(r + step);
     const bool live = r < rows;
