@@ -1,6 +1,7 @@
 // finetune_lib.hip -- C ABI of libfinetune.so: argument checks, kernel selection, launches.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "finetune.h"
@@ -22,6 +23,11 @@ int by_dtype(int64_t dtype, F f) {
     default: return f(F16{});
   }
 }
+
+template <class T>
+struct TypeOf {
+  using type = T;
+};
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -466,13 +472,14 @@ int launch_policy_step(const finetune_logits* in, const PolicyCall& c, float sca
 
 // ---- gradient tensors -----------------------------------------------------
 
-// f(table, chunks) for tables of up to kClipTensors tensors, the chunks of a
-// launch below 2^24, laid out along the lines of the tensors in (OUT: out);
-// OUT: the last tensor first.
-template <bool OUT, class F>
+// f(table, chunks) for tables of up to Table::kMost tensors, the chunks of a
+// launch below 2^24, laid out along the lines of the tensors read (BACK:
+// written); BACK: the last tensor first.
+template <class Table, bool BACK, class F>
 int for_tables(const finetune_tensor* t, int64_t n, F f) {
-  constexpr int64_t kMost = int64_t(1) << 23;
-  ClipTable table;
+  constexpr int64_t kMost = int64_t(1) << 23, kEntryChunks = int64_t(1) << 16;
+  static_assert(kEntryChunks * kClipBytes / 2 < kClipEntry, "an entry's elements fit its count");
+  Table table;
   table.n = 0;
   table.first[0] = 0;
   auto flush = [&]() {
@@ -482,25 +489,24 @@ int for_tables(const finetune_tensor* t, int64_t n, F f) {
     return st;
   };
   for (int64_t at = 0; at < n; ++at) {
-    const finetune_tensor& x = t[OUT ? n - 1 - at : at];
+    const finetune_tensor& x = t[BACK ? n - 1 - at : at];
     int64_t left = x.count;
     const int size = static_cast<int>(dtype_bytes(static_cast<int>(x.dtype)));
     const int64_t per = kClipBytes / size;
     const char* g = static_cast<const char*>(x.grad);
     char* o = static_cast<char*>(x.out);
     while (left > 0) {
-      const int64_t take = std::min<int64_t>(left, kMost * per);
-      const int64_t chunks = ceil_div(take + clip_lead(OUT ? o : g, size), per);
+      const int64_t take = std::min<int64_t>(left, kEntryChunks * per);
+      const int64_t chunks = ceil_div(take + clip_lead(BACK ? o : g, size), per);
       const int k = table.n++;
       table.in[k] = g;
-      table.out[k] = o;
-      table.count[k] = take;
-      table.dtype[k] = static_cast<int8_t>(x.dtype);
+      if constexpr (Table::kApart) table.to[k] = o;
+      table.count[k] = static_cast<uint32_t>(x.dtype) * kClipEntry + static_cast<uint32_t>(take);
       table.first[k + 1] = table.first[k] + static_cast<int>(chunks);
       left -= take;
       g += take * size;
       if (o) o += take * size;
-      if (table.n == kClipTensors || table.first[table.n] >= kMost) {
+      if (table.n == Table::kMost || table.first[table.n] >= kMost) {
         const int st = flush();
         if (st != RDFFT_OK) return st;
       }
@@ -515,7 +521,7 @@ unsigned clip_grid(int chunks) { return static_cast<unsigned>(std::min(chunks, k
 struct ClipShape {
   int64_t parts = 0, chunks = 0;
   ClipShape(const finetune_tensor* t, int64_t n) {
-    for_tables<false>(t, n, [&](const ClipTable&, int c) {
+    for_tables<ClipHere, false>(t, n, [&](const ClipHere&, int c) {
       parts += clip_grid(c);
       chunks += c;
       return static_cast<int>(RDFFT_OK);
@@ -534,7 +540,7 @@ int launch_squares(const finetune_tensor* t, int64_t n, const ClipShape& shape, 
                    hipStream_t s) {
   int64_t keep = shape.chunks * kClipBytes * (again ? 2 : 1);
   keep = !past_caches(keep) ? 0 : again ? shape.chunks - kClipKeepChunks : shape.chunks;
-  return for_tables<false>(t, n, [&](const ClipTable& table, int chunks) {
+  return for_tables<ClipHere, false>(t, n, [&](const ClipHere& table, int chunks) {
     const int here = static_cast<int>(std::max<int64_t>(std::min<int64_t>(keep, chunks), 0));
     hipLaunchKernelGGL((grad_square_kernel), dim3(clip_grid(chunks)), dim3(kClipThreads), 0, s, table, here, partial);
     partial += clip_grid(chunks);
@@ -551,14 +557,19 @@ int launch_norm(const double* partial, int64_t parts, float* norm, hipStream_t s
 // the launches over the tables, the first of them with the norm's address
 int launch_scale(const finetune_tensor* t, int64_t n, const ClipShape& shape, const double* partial, double max_norm,
                  double eps, float* norm, hipStream_t s) {
-  return for_tables<true>(t, n, [&](const ClipTable& table, int chunks) {
-    by_stream(past_caches(2 * shape.chunks * kClipBytes), [&](auto stream) {
-      hipLaunchKernelGGL((grad_scale_kernel<decltype(stream)::value>), dim3(clip_grid(chunks)), dim3(kClipThreads), 0,
-                         s, table, partial, shape.parts, max_norm, eps, norm);
+  const auto over = [&](auto kind) {
+    using Table = typename decltype(kind)::type;
+    return for_tables<Table, true>(t, n, [&](const Table& table, int chunks) {
+      by_stream(past_caches(2 * shape.chunks * kClipBytes), [&](auto stream) {
+        hipLaunchKernelGGL((grad_scale_kernel<Table, decltype(stream)::value>), dim3(clip_grid(chunks)),
+                           dim3(kClipThreads), 0, s, table, partial, shape.parts, max_norm, eps, norm);
+      });
+      norm = nullptr;
+      return launch_status();
     });
-    norm = nullptr;
-    return launch_status();
-  });
+  };
+  const auto apart = [](const finetune_tensor& x) { return x.count > 0 && x.out != x.grad; };
+  return std::any_of(t, t + n, apart) ? over(TypeOf<ClipApart>{}) : over(TypeOf<ClipHere>{});
 }
 
 }  // namespace

@@ -14,19 +14,29 @@ namespace finetune {
 constexpr int kClipThreads = 256;
 constexpr int kClipBytes = 16384;   // of a chunk, the unit of work: four 16-byte pieces a thread
 constexpr int kClipPieces = kClipBytes / 16 / kClipThreads;
-constexpr int kClipTensors = 128;   // tensors of one launch (the table travels in the kernel's arguments)
 constexpr int kClipGroups = 2048;   // workgroups of a launch at most: 8 a compute unit, and one partial sum each
+constexpr uint32_t kClipEntry = 1u << 30;  // elements of a table's entry stay below this
 constexpr int kClipLine = 128;      // chunks start at addresses divisible by this
 
+// The tensors of one launch: the table travels in the kernel's arguments, as
+// many as fit 4 KB with them.  APART: out is elsewhere.  An entry's elements
+// (below 2^30) and its type share a word: with 8 bytes for the count and a byte
+// for the type a table held 128, and 288 tensors, three launches a pass, took
+// 38 us, 30 us with these.
+template <int MOST, bool APART>
 struct ClipTable {
-  const void* in[kClipTensors];
-  void* out[kClipTensors];
-  int64_t count[kClipTensors];
-  int first[kClipTensors + 1];  // first chunk of each tensor within the launch
-  int8_t dtype[kClipTensors];
+  static constexpr int kMost = MOST;
+  static constexpr bool kApart = APART;
+  const void* in[MOST];
+  void* to[APART ? MOST : 1];
+  uint32_t count[MOST];  // type * 2^30 + elements
+  int first[MOST + 1];   // first chunk of each tensor within the launch
   int n;
+  __host__ __device__ void* out(int i) const { return APART ? to[APART ? i : 0] : const_cast<void*>(in[i]); }
 };
-static_assert(sizeof(ClipTable) <= 3800, "kernel arguments are limited to 4 KB");
+using ClipHere = ClipTable<232, false>;
+using ClipApart = ClipTable<156, true>;
+static_assert(sizeof(ClipHere) <= 3800 && sizeof(ClipApart) <= 3800, "kernel arguments are limited to 4 KB");
 
 // Elements between the last 128-byte line before p and p: chunk k of a tensor
 // holds its elements [k N - lead, (k + 1) N - lead), N = 16 KB of them, so that
@@ -37,7 +47,8 @@ __host__ __device__ inline int clip_lead(const void* p, int size) {
 
 // The tensor that chunk c belongs to, at or after tensor i: the last whose
 // first chunk is <= c.
-__device__ __forceinline__ int tensor_of(const ClipTable& t, int c, int i) {
+template <class Table>
+__device__ __forceinline__ int tensor_of(const Table& t, int c, int i) {
   if (c < t.first[i + 1]) return i;
   int lo = i + 1, hi = t.n;
   while (hi - lo > 1) {
@@ -54,8 +65,8 @@ __device__ __forceinline__ int tensor_of(const ClipTable& t, int c, int i) {
 // workgroup, dealt out in turn so that all workgroups read one region at a
 // time.  BACK: a tensor's last chunk first.  `at` of a tensor is the pointer
 // whose lines the chunks follow.
-template <bool BACK, class At, class F>
-__device__ __forceinline__ void for_chunks(const ClipTable& t, At at, F f) {
+template <bool BACK, class Table, class F>
+__device__ __forceinline__ void for_chunks(const Table& t, F f) {
   const int chunks = t.first[t.n];
   int i = 0;
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
@@ -64,12 +75,14 @@ __device__ __forceinline__ void for_chunks(const ClipTable& t, At at, F f) {
       using T = typename decltype(io)::T;
       constexpr int N = kClipBytes / sizeof(T);
       const int64_t k = BACK ? t.first[i + 1] - 1 - c : c - t.first[i];
-      const int64_t a = k * N - clip_lead(at(i), sizeof(T)), b = a + N, n = t.count[i];
-      f(io, static_cast<const T*>(t.in[i]), static_cast<T*>(t.out[i]), a > 0 ? a : 0, b < n ? b : n, a, c);
+      const void* lines = BACK ? t.out(i) : t.in[i];
+      const int64_t a = k * N - clip_lead(lines, sizeof(T)), b = a + N, n = t.count[i] & (kClipEntry - 1);
+      f(io, static_cast<const T*>(t.in[i]), static_cast<T*>(t.out(i)), a > 0 ? a : 0, b < n ? b : n, a, c);
     };
-    if (t.dtype[i] == 0)
+    const int type = t.count[i] / kClipEntry;
+    if (type == 0)
       with(F32{});
-    else if (t.dtype[i] == 1)
+    else if (type == 1)
       with(Bf16{});
     else
       with(F16{});
@@ -98,12 +111,11 @@ __device__ __forceinline__ void for_pieces(int64_t origin, int64_t begin, int64_
 
 // partial[workgroup] = the sum of squares of its chunks; those below `keep` are
 // read past the caches
-__global__ void __launch_bounds__(kClipThreads) grad_square_kernel(ClipTable t, int keep, double* partial) {
+__global__ void __launch_bounds__(kClipThreads) grad_square_kernel(ClipHere t, int keep, double* partial) {
   __shared__ double s[kClipThreads / kWave];
   double sum[2] = {0.0, 0.0};
   for_chunks<false>(
-      t, [&](int i) { return t.in[i]; },
-      [&](auto io, const auto* g, auto*, int64_t begin, int64_t end, int64_t origin, int c) {
+      t, [&](auto io, const auto* g, auto*, int64_t begin, int64_t end, int64_t origin, int c) {
         using Io = decltype(io);
         constexpr int V = Io::kVec;
         typename Io::Vec raw[kClipPieces] = {};  // pieces that are not there add zero
@@ -147,17 +159,16 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const double* p
 // itself (16 KB from L2 at most a launch of squares) instead of waiting for a
 // kernel that does.  The tables come in reverse and so do a tensor's chunks:
 // what the squares read last is still in the 256 MB cache.
-template <bool STREAM>
+template <class Table, bool STREAM>
 __global__ void __launch_bounds__(kClipThreads)
-    grad_scale_kernel(ClipTable t, const double* partial, int64_t parts, double max_norm, double eps, float* norm) {
+    grad_scale_kernel(Table t, const double* partial, int64_t parts, double max_norm, double eps, float* norm) {
   __shared__ double s[kClipThreads / kWave];
   const double a = norm_of(partial, parts, s);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = static_cast<float>(a);
   const double q = max_norm / (a + eps);
   const float f = q > 1.0 ? 1.0f : static_cast<float>(q);
   for_chunks<true>(
-      t, [&](int i) { return static_cast<const void*>(t.out[i]); },
-      [&](auto io, const auto* g, auto* o, int64_t begin, int64_t end, int64_t origin, int) {
+      t, [&](auto io, const auto* g, auto* o, int64_t begin, int64_t end, int64_t origin, int) {
         using Io = decltype(io);
         constexpr int V = Io::kVec;
         if (f == 1.0f && g == o) return;  // nothing to change in place

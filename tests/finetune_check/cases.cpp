@@ -356,7 +356,7 @@ int main(int argc, char** argv) {
   clip_case({33, 8192, 7}, 2, 2, true, 1.0);
   clip_case({100, 50}, 0, 0, true, 1e9);
   std::vector<int64_t> many;
-  for (int64_t i = 0; i < (small ? 131 : 300); ++i) many.push_back(i % 7);
+  for (int64_t i = 0; i < (small ? 240 : 300); ++i) many.push_back(i % 7);
   clip_case(many, 1, 1, false, 1.0);  // several tables
   std::printf("ok %ld %ld\n", cases, emu::launches);
   return 0;

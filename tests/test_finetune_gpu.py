@@ -774,3 +774,42 @@ def test_many_rows_either_side_of_a_wave_a_row(t, v, dtype):
     buf = xd.clone()
     bcl.preference_loss_step(buf, ld, ref, kind="ipo", average=True, dlogits=buf)
     assert torch.equal(buf, d)
+
+
+@pytest.mark.parametrize("n", [156, 157, 232, 233, 320])
+def test_clip_either_side_of_a_table(n):
+    sizes = [1 + 37 * k % 211 for k in range(n)]
+    dtypes = [("f32", "bf16", "f16")[k % 3] for k in range(n)]
+    ts, refs = tensors((90, n), [(s,) for s in sizes], dtypes)
+    norm0, want = fo.clip(refs, 0.5)
+    out = [torch.full_like(t, float("nan")) if k % 2 else t.clone() for k, t in enumerate(ts)]
+    norm = bcl.clip_grad_norm(ts, 0.5, out=out)
+    within(f64(norm), norm0, 4 * U * norm0)
+    for o, w, dt in zip(out, want, dtypes):
+        within(f64(o), w, store_err(w, dt) + 4 * U * np.abs(w))
+    some = [t.clone() if k % 2 else t for k, t in enumerate(ts)]  # in place among others elsewhere
+    to = [o if k % 2 else torch.empty_like(o) for k, o in enumerate(some)]
+    assert torch.equal(bcl.clip_grad_norm(some, 0.5, out=to), norm)
+    assert torch.equal(bcl.clip_grad_norm(ts, 0.5), norm)
+    for t, o, p in zip(ts, out, to):
+        assert torch.equal(t, o) and torch.equal(p, o)
+
+
+def test_clip_a_tensor_past_one_entry():
+    # 1.07 GB of bf16, an odd element in: several entries of the table, chunks on lines throughout
+    n = (1 << 29) + 11
+    g = torch.Generator(device=DEV).manual_seed(91)
+    buf = torch.randn(n + 1, generator=g, device=DEV, dtype=torch.bfloat16)
+    t = buf[1:]
+    total = sum(float(t[a: a + (1 << 26)].double().square().sum()) for a in range(0, n, 1 << 26))
+    first = buf[:1].clone()
+    out = torch.empty_like(t)
+    norm = bcl.clip_grad_norm([t], 100.0, out=[out])
+    within(f64(norm), np.sqrt(total), 4 * U * np.sqrt(total))
+    f = min(1.0, 100.0 / (np.sqrt(total) + 1e-6))
+    for a in range(0, n, 1 << 26):
+        w = t[a: a + (1 << 26)].double() * f
+        # a bfloat16 rounding (2^-8) and the factor's and the product's in 24 bits; the least subnormal's half
+        assert bool(((out[a: a + (1 << 26)].double() - w).abs() <= (2.0**-8 + 4 * U) * w.abs() + 2.0**-134).all())
+    bcl.clip_grad_norm([t], 100.0)
+    assert torch.equal(t, out) and torch.equal(buf[:1], first)
