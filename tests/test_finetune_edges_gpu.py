@@ -1,0 +1,64 @@
+"""GPU tests of the fine-tuning operators at the edges of fp32: rows of logits
+with a common offset or at a type's lowest value, log-ratios that are infinite,
+and normalised rows whose mean is large.
+
+With u = 2^-24: exp(x - lse) takes one rounding of x - lse, one of its product
+with log2(e) and the constant's own (0.22 u), so the exponent errs by less than
+2.5 u |x - lse| and the value by that and a few roundings of its own; 3 u |x -
+lse| + 8 u is asked for.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import block_circulant_layers_amd as bcl
+from tests.finetune_util import IGNORE, STORE, TORCH, U, f64, rng, stored, within
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+LOWEST = {dt: float(torch.finfo(TORCH[dt]).min) for dt in TORCH}
+
+
+def check_gradient(got, x, lab, lse, g, dtype):
+    """got against g (onehot - exp(x - lse)) in float64 at the same float32 lse."""
+    x, lse, g = f64(x), f64(lse)[..., None], np.asarray(g, np.float64)[..., None]
+    d = x - lse
+    p = np.where(lab[..., None] == IGNORE, 0.0, np.exp(np.where(lab[..., None] == IGNORE, 0.0, d)))
+    hot = np.arange(x.shape[-1]) == lab[..., None]
+    want = np.where(lab[..., None] == IGNORE, 0.0, g * (hot - p))
+    s, tiny = STORE[dtype]
+    within(f64(got), want, s * np.abs(want) * 1.01 + tiny + np.abs(g) * p * (3 * np.abs(d) + 8) * U + 4 * U * np.abs(want)
+           + np.abs(g) * 2.0**-125)
+
+
+def offset_case(n, t, v, offset, dtype):
+    """Logits around `offset` ("lowest": nothing but the type's lowest value) and labels, some masked."""
+    r = rng(200, n, t, v)
+    lab = r.integers(0, v, size=(n, t))
+    lab[r.random((n, t)) < 0.2] = IGNORE
+    lab[:, 0] = v // 2  # an unmasked position in every sequence
+    x = np.full((n, t, v), LOWEST[dtype]) if offset == "lowest" else offset + 3.0 * r.standard_normal((n, t, v))
+    return stored(x, dtype)[0].to(DEV), torch.from_numpy(lab).to(DEV), lab
+
+
+OFFSETS = [("f32", o) for o in (0.0, 100.0, 1e4, -1e4, 1e10, -1e10, 3e38, "lowest")]
+OFFSETS += [("bf16", o) for o in (100.0, 1e4, -1e10, "lowest")] + [("f16", o) for o in (100.0, -1e4, "lowest")]
+
+
+@pytest.mark.parametrize("dtype,offset", OFFSETS)
+@pytest.mark.parametrize("n,t,v", [(2, 3, 601), (2, 2, 9001), (2, 300, 130), (2, 260, 4099)])
+def test_gradient_of_rows_with_an_offset(n, t, v, dtype, offset):
+    x, labels, lab = offset_case(n, t, v, offset, dtype)
+    logp, lse = bcl.token_logprob(x, labels)
+    assert bool(lse.isfinite().all())
+    g = torch.from_numpy(rng(201, n, t).standard_normal((n, t))).to(DEV, torch.float32)
+    check_gradient(bcl.token_logprob_bwd(x, labels, lse, g), x, lab, lse, f64(g), dtype)
+    r, d = bcl.preference_loss_step(x, labels, logp - 0.1, beta=0.3, kind="ipo", average=True)
+    check_gradient(d, x, lab, r.lse, np.repeat(f64(r.slope)[:, None], t, 1), dtype)
+    adv = torch.tensor([1.0, -0.5], device=DEV)
+    p, d = bcl.policy_loss_step(x, labels, logp, adv, reduction="sum")
+    assert bool(p.lse.isfinite().all())
+    check_gradient(d, x, lab, p.lse, f64(p.slope), dtype)
