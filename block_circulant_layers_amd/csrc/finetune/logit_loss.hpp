@@ -383,9 +383,10 @@ __device__ __forceinline__ Pair pair_of(const JoinParts<Io>& join, const int64_t
   const double h = q.ratio[0] - q.ratio[1], z = how.beta * h, e = how.smoothing;
   double dh;
   if (how.kind == 0) {
-    const double t = exp(-fabs(z)), up = (z < 0.0 ? z : 0.0) - log1p(t);  // log sigma(z); log sigma(-z) = up - z
-    const double big = 1.0 / (1.0 + t), small = t * big;                  // sigma(|z|) and sigma(-|z|)
-    q.loss = -(1.0 - e) * up - e * (up - z);
+    const double t = exp(-fabs(z)), low = log1p(t);
+    const double up = (z < 0.0 ? z : 0.0) - low, down = (z > 0.0 ? -z : 0.0) - low;  // log sigma(z) and log sigma(-z)
+    const double big = 1.0 / (1.0 + t), small = t * big;                             // sigma(|z|) and sigma(-|z|)
+    q.loss = -(1.0 - e) * up - (e > 0.0 ? e * down : 0.0);  // both may be infinite
     dh = z < 0.0 ? -how.beta * ((1.0 - e) * big - e * small) : -how.beta * ((1.0 - e) * small - e * big);
   } else if (how.kind == 1) {
     q.loss = z < 1.0 ? 1.0 - z : z >= 1.0 ? 0.0 : z;  // the last: NaN

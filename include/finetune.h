@@ -130,7 +130,7 @@ int token_logprob(const finetune_logits* in, float* logp, float* lse, void* ws, 
 int token_logprob_bwd(const finetune_logits* in, const float* lse, const float* dlogp, const finetune_dlogits* out,
                       void* stream);
 
-#define PREFERENCE_SIGMOID 0 /* -(1-e) log sigma(b h) - e log sigma(-b h) */
+#define PREFERENCE_SIGMOID 0 /* -(1-e) log sigma(b h) - e log sigma(-b h); e = 0: the first term alone */
 #define PREFERENCE_HINGE 1   /* max(0, 1 - b h) */
 #define PREFERENCE_IPO 2     /* (h - 1/(2 b))^2 */
 

@@ -62,3 +62,26 @@ def test_gradient_of_rows_with_an_offset(n, t, v, dtype, offset):
     p, d = bcl.policy_loss_step(x, labels, logp, adv, reduction="sum")
     assert bool(p.lse.isfinite().all())
     check_gradient(d, x, lab, p.lse, f64(p.slope), dtype)
+
+
+@pytest.mark.parametrize("n_pos", [1, 300])  # rows fewer and more than a step's gradient works the slopes out for
+@pytest.mark.parametrize("smoothing", [0.0, 0.1])
+def test_preference_of_infinite_log_ratios(smoothing, n_pos):
+    # pair 0: the chosen label's logit is -inf, z = -inf; pair 1: the rejected one's, z = +inf; pair 2: none
+    beta, v = 0.25, 50
+    x = torch.zeros(6, n_pos, v, device=DEV)
+    lab = torch.full((6, n_pos), 7, dtype=torch.int64, device=DEV)
+    x[0, 0, 7] = x[4, 0, 7] = float("-inf")
+    ref = torch.zeros(6, n_pos, device=DEV)
+    r, d = bcl.preference_loss_step(x, lab, ref, beta=beta, label_smoothing=smoothing)
+    f = bcl.preference_loss_fwd(x, lab, ref, beta=beta, label_smoothing=smoothing)
+    e = smoothing
+    slope = [-beta * (1 - e), beta * e, -beta * (0.5 - e)]  # d loss / d h at z = -inf, +inf and 0
+    for got in (r, f):
+        loss = f64(got.loss)
+        assert loss[0] == np.inf and loss[1] == (np.inf if e else 0.0) and abs(loss[2] - np.log(2.0)) <= 4 * U
+        within(f64(got.slope), np.array([*slope, *[-s for s in slope]]), 2 * U)
+    assert bool(d.isfinite().all()) and torch.equal(d[0, 0, 7], r.slope[0])
+    # the separate backward gives the same
+    two = bcl.preference_loss_bwd(x, lab, f.lse, f.slope, torch.ones(3, device=DEV))
+    assert torch.equal(two, d)
