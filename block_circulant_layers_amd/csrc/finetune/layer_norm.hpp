@@ -221,31 +221,32 @@ __global__ void __launch_bounds__(norm_wg(T))
     const float mu = nm, rs = nr;
     if (AHEAD && r + step < rows) fetch(r + step);
     const bool live = r < rows;
+    // With q = dy rstd and t = x - mean, hat enters as q t: A = sum q w and C =
+    // rstd sum q w t give dx = q w - A / d - t rstd C / d.  (dy hat instead is as
+    // many instructions, but where a row ends, at x = dy = 0, hat = -mean rstd may
+    // be infinite, and 0 times it NaN.)
     float a = 0.0f, c = 0.0f;
 #pragma unroll
     for (int k = 0; k < E; ++k) {
-      const float g = cg.at(k), hat = (cx.at(k) - mu) * rs;
+      const float g = cg.at(k), q = g * rs, t = cx.at(k) - mu;
       // columns past the row hold g = 0; a round without a row adds nothing
-      a += g * wr[k];
-      c += g * wr[k] * hat;
+      a += q * wr[k];
+      c += q * wr[k] * t;
       if constexpr (IN_LDS) {
-        mine[k * T] += g * hat;
+        mine[k * T] += q * t;
         mine[(E + k) * T] += g;
       } else if (live) {
-        dw[k] += g * hat;
+        dw[k] += q * t;
         db[k] += g;
       }
     }
     if (dx) {
       a = group_sum<T>(a, s[turn][0]) / n;
-      c = group_sum<T>(c, s[turn][1]) / n;
+      c = rs * (group_sum<T>(c, s[turn][1]) / n);
       if (live) {
         float v[E];
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          const float hat = (cx.at(k) - mu) * rs;
-          v[k] = rs * (cg.at(k) * wr[k] - a - hat * c);
-        }
+        for (int k = 0; k < E; ++k) v[k] = cg.at(k) * rs * wr[k] - a - (cx.at(k) - mu) * rs * c;
         Row::store(dx + r * dxs, d, v);
       }
     }

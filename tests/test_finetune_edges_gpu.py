@@ -85,3 +85,23 @@ def test_preference_of_infinite_log_ratios(smoothing, n_pos):
     # the separate backward gives the same
     two = bcl.preference_loss_bwd(x, lab, f.lse, f.slope, torch.ones(3, device=DEV))
     assert torch.equal(two, d)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [3, 100, 128, 1000, 1500, 4090, 5001, 16380, 16384])
+def test_layer_norm_bwd_of_constant_rows_with_a_large_mean(d, dtype):
+    # hat is 0 all along the row; (0 - mean) rstd, what a place past the row's end would give, is past fp32's range
+    r = rng(210, d)
+    mean = stored(np.array([1e37, -1e37, 3.0]), dtype)[0].to(DEV)
+    x = mean[:, None].expand(3, d).contiguous()
+    dy, dyr = stored(r.standard_normal((3, d)), dtype)
+    w, wr = stored(1.0 + 0.2 * r.standard_normal(d), "f32")
+    rstd = torch.full((3,), 316.0, device=DEV)
+    dx, dw, db = bcl.layer_norm_bwd(x, w.to(DEV), mean.float(), rstd, dy.to(DEV))
+    g = dyr * wr
+    want = 316.0 * (g - g.mean(-1, keepdims=True))
+    s, tiny = STORE[dtype]
+    e = (d / 64 + 24) * U  # a sum's error of its magnitudes, and the other roundings
+    within(f64(dx), want, s * np.abs(want) * 1.01 + tiny + 316.0 * e * (np.abs(g) + np.abs(g).mean(-1, keepdims=True)))
+    assert not dw.any()
+    within(f64(db), dyr.sum(0), 8 * U * np.abs(dyr).sum(0))
