@@ -62,6 +62,15 @@ float* f32(const char* name, const Opt& t, at::IntArrayRef shape, const Tensor& 
   return t ? f32(name, *t, shape, like) : nullptr;
 }
 
+// Counts a write to a tensor of the caller's, which torch cannot see: autograd
+// refuses a backward that needs the values from before.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(const Opt& t) {
+  if (t) written(*t);
+}
+
 Tensor new_f32(at::IntArrayRef shape, const Tensor& like) { return at::empty(shape, like.options().dtype(at::kFloat)); }
 
 // Several small arrays of one call in one allocation: each an allocation of its
@@ -143,6 +152,7 @@ std::tuple<Tensor, Tensor, Tensor> layer_norm_fwd_(const Tensor& x, const Opt& w
   check("layer_norm_fwd",
         layer_norm_fwd(x.data_ptr(), w, b, out.data_ptr(), static_cast<float*>(mean.data_ptr()),
                        static_cast<float*>(rstd.data_ptr()), r.rows, r.d, r.stride, ys, eps, code, stream_of(x)));
+  written(y);
   return {out, mean, rstd};
 }
 
@@ -175,6 +185,9 @@ std::tuple<Opt, Opt, Opt> layer_norm_bwd_(const Tensor& x, const Opt& weight, co
         layer_norm_bwd(x.data_ptr(), w, m, s, dy.data_ptr(), ptr(odx), static_cast<float*>(ptr(odw)),
                        static_cast<float*>(ptr(odb)), work ? work->p() : nullptr, work ? work->bytes() : 0, r.rows,
                        r.d, r.stride, dys, dxs, code, stream_of(x)));
+  if (need_dx) written(dx);
+  if (need_dw) written(dw);
+  if (need_db) written(db);
   return {odx, odw, odb};
 }
 
@@ -246,6 +259,7 @@ Tensor token_logprob_bwd_(const Tensor& logits, const Tensor& labels, const Tens
   Tensor out = dlogits_of(logits, dlogits);
   const finetune_dlogits args = dlogits_args(out);
   check("token_logprob_bwd", token_logprob_bwd(&in, l, d, &args, stream_of(logits)));
+  written(dlogits);
   return out;
 }
 
@@ -273,6 +287,7 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor, Opt> preference_loss_(
   check("preference_loss_step",
         preference_loss_step(&in, ref, &how, *scale, ptr(loss), ptr(ratio), ptr(logp), ptr(lse), ptr(slope), &args,
                              work.p(), work.bytes(), stream_of(logits)));
+  written(dlogits);
   return {loss, ratio, logp, lse, slope, out};
 }
 
@@ -286,6 +301,7 @@ Tensor preference_loss_bwd_(const Tensor& logits, const Tensor& labels, const Te
   Tensor out = dlogits_of(logits, dlogits);
   const finetune_dlogits args = dlogits_args(out);
   check("preference_loss_bwd", preference_loss_bwd(&in, l, s, d, &args, stream_of(logits)));
+  written(dlogits);
   return out;
 }
 
@@ -319,6 +335,7 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor, Opt> policy_loss_(
   check("policy_loss_step",
         policy_loss_step(&in, old, ref, adv, &how, *scale, ptr(loss), ptr(logp), ptr(lse), ptr(slope), &args,
                          work.p(), work.bytes(), stream_of(logits)));
+  written(dlogits);
   return {loss, kl, logp, lse, slope, out};
 }
 
@@ -333,6 +350,7 @@ Tensor policy_loss_bwd_(const Tensor& logits, const Tensor& labels, const Tensor
   Tensor out = dlogits_of(logits, dlogits);
   const finetune_dlogits args = dlogits_args(out);
   check("policy_loss_bwd", policy_loss_bwd(&in, l, s, d, &args, stream_of(logits)));
+  written(dlogits);
   return out;
 }
 
@@ -386,11 +404,15 @@ Tensor clip_grad_norm_(const py::list& grad_list, std::optional<double> max_norm
   int64_t need = 0;
   check("grad_norm_workspace", grad_norm_workspace(table.data(), n, &need));
   const Workspace work(first, need, ws);
-  if (max_norm)
+  if (max_norm) {
     check("clip_grad_norm", clip_grad_norm(table.data(), n, *max_norm, eps, ptr(result), work.p(), work.bytes(),
                                            stream_of(first)));
-  else
+    const TensorList& changed = out ? *out : grads;
+    for (size_t i = 0; i < changed.size(); ++i) written(changed[i]);
+  } else {
     check("grad_norm", grad_norm(table.data(), n, ptr(result), work.p(), work.bytes(), stream_of(first)));
+  }
+  written(norm);
   return result;
 }
 

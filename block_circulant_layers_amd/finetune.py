@@ -14,7 +14,9 @@ by the module ``lib/_finetune_host.so``), autograd functions on them
 
 Calls only enqueue work on the current stream of the tensors' device, or on
 ``stream``, where their temporary workspace is then allocated too.  There is
-no CPU path.  Weights and statistics are float32; activations and logits may be
+no CPU path.  A tensor of the caller's that a call overwrites counts as modified
+in place, so that autograd refuses a backward that still needs its old values.
+Weights and statistics are float32; activations and logits may be
 float32, bfloat16 or float16.  ``ws`` is a workspace to use instead of a new
 one, of at least the bytes that the C ABI's queries give.
 """
@@ -312,9 +314,11 @@ class _LogitLoss(torch.autograd.Function):
     def forward(ctx, logits, labels, fwd, bwd, inplace):
         logits = _logits_layout(logits)
         outs, lse, slope = fwd(logits, labels)
-        # a buffer that the backward itself overwrites is kept beside the saved tensors, good for one backward
+        # a buffer that the backward itself overwrites is kept beside the saved tensors, good for one backward, with
+        # the version that autograd would otherwise check
         ctx.save_for_backward(labels, lse, slope, None if inplace else logits)
         ctx.logits, ctx.bwd = logits if inplace else None, bwd
+        ctx.version = logits._version if inplace and not logits.is_inference() else None
         ctx.mark_non_differentiable(*outs[1:])
         return outs if len(outs) > 1 else outs[0]
 
@@ -328,13 +332,18 @@ class _LogitLoss(torch.autograd.Function):
             ctx.logits = None
             if logits is None:
                 raise RuntimeError("the loss was backpropagated before (its gradient replaced the logits)")
+            if logits._version != ctx.version:
+                raise RuntimeError("the logits were modified after the loss was computed from them (by another loss's "
+                                   "inplace gradient, perhaps)")
         d = ctx.bwd(logits, labels, lse, slope, dloss.float().contiguous(), dlogits=target)
         return d, None, None, None, None
 
 
 def token_logp(logits: torch.Tensor, labels: torch.Tensor, inplace: bool = False) -> torch.Tensor:
     """Differentiable token log-probabilities (sequences, positions) of labels;
-    ``inplace``: the backward writes the gradient over the logits."""
+    ``inplace``: the backward writes the gradient over the logits.  What else in
+    the graph needs them, or another part of the tensor they are a view of,
+    raises if its backward comes later."""
 
     def fwd(x, y):
         logp, lse = token_logprob(x, y)
@@ -351,7 +360,7 @@ def preference_loss(logits: torch.Tensor, labels: torch.Tensor, ref_logp: torch.
                     inplace: bool = False):
     """Differentiable preference loss: returns (loss of each pair, log-ratio of
     each sequence); ``inplace``: the backward writes the gradient over the
-    logits."""
+    logits, as for :func:`token_logp`."""
 
     def fwd(x, y):
         r = preference_loss_fwd(x, y, ref_logp.contiguous(), beta, kind, label_smoothing, average)
@@ -364,7 +373,7 @@ def policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tens
                 ref_logp: torch.Tensor | None = None, clip_low: float = 0.2, clip_high: float = 0.2,
                 kl_coef: float = 0.0, reduction: str = "token", inplace: bool = False):
     """Differentiable clipped policy loss: returns (loss, kl); ``inplace``: the
-    backward writes the gradient over the logits."""
+    backward writes the gradient over the logits, as for :func:`token_logp`."""
 
     def fwd(x, y):
         r = policy_loss_fwd(x, y, old_logp.contiguous(), advantages.contiguous(),
