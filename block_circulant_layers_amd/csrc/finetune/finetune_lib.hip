@@ -415,22 +415,24 @@ int launch_policy(const finetune_logits* in, const PolicyCall& c, float* stats, 
 
 // The step with the rows held in registers, where there are rows enough to fill
 // the chip and a row fits a workgroup: f(threads, pieces a thread), and whether
-// there was such a shape.
+// there was such a shape.  A workgroup takes one row (it has no registers to
+// spare for a loop's), and HIP launches fewer than 2^32 threads: batches past
+// that take the kernels that walk over the rows.
+constexpr int64_t kLaunchThreads = (int64_t(1) << 32) - 1;
 template <class F>
 bool by_held_row(const finetune_logits* in, F f) {
   const int64_t pieces = in->vocab / (in->dtype == RDFFT_F32 ? 4 : 8);
+  const auto with = [&](auto nt, auto r) {
+    if (logit_rows(in) > kLaunchThreads / decltype(nt)::value) return false;
+    f(nt, r);
+    return true;
+  };
   if (logit_rows(in) < kWantGroups) return false;
-  if (pieces <= 64 * 8)
-    f(std::integral_constant<int, 64>{}, std::integral_constant<int, 8>{});
-  else if (pieces <= 256 * 8)
-    f(std::integral_constant<int, 256>{}, std::integral_constant<int, 8>{});
-  else if (pieces <= 512 * 16)
-    f(std::integral_constant<int, 512>{}, std::integral_constant<int, 16>{});
-  else if (pieces <= 1024 * 16)
-    f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 16>{});
-  else
-    return false;
-  return true;
+  if (pieces <= 64 * 8) return with(std::integral_constant<int, 64>{}, std::integral_constant<int, 8>{});
+  if (pieces <= 256 * 8) return with(std::integral_constant<int, 256>{}, std::integral_constant<int, 8>{});
+  if (pieces <= 512 * 16) return with(std::integral_constant<int, 512>{}, std::integral_constant<int, 16>{});
+  if (pieces <= 1024 * 16) return with(std::integral_constant<int, 1024>{}, std::integral_constant<int, 16>{});
+  return false;
 }
 
 int launch_policy_step(const finetune_logits* in, const PolicyCall& c, float scale, float* stats, float* logp,

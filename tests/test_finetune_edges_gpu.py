@@ -105,3 +105,27 @@ def test_layer_norm_bwd_of_constant_rows_with_a_large_mean(d, dtype):
     within(f64(dx), want, s * np.abs(want) * 1.01 + tiny + 316.0 * e * (np.abs(g) + np.abs(g).mean(-1, keepdims=True)))
     assert not dw.any()
     within(f64(db), dyr.sum(0), 8 * U * np.abs(dyr).sum(0))
+
+
+def test_policy_step_of_more_rows_than_a_launch_has_threads_for():
+    # 2^26 + 5 rows, which at a wave a row is past the 2^32 threads that one launch may have
+    t, v = (1 << 26) + 5, 16
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.randn(1, t, v, generator=g, device=DEV, dtype=torch.bfloat16)
+    lab = torch.randint(0, v, (1, t), generator=g, device=DEV)
+    lab[0, ::7] = IGNORE
+    old = torch.full((1, t), -2.5, device=DEV)
+    adv = torch.ones(1, device=DEV)
+    r, d = bcl.policy_loss_step(x, lab, old, adv, reduction="token")
+    live = lab[0] != IGNORE
+    ratio = (r.logp[0].double() - old[0].double()).exp()
+    each = -torch.minimum(ratio, ratio.clamp(0.8, 1.2))
+    want = float(torch.where(live, each, 0.0).sum() / live.sum())
+    within(float(r.loss), want, 4 * U * abs(want))
+    at = torch.cat([torch.randint(0, t, (4000,), generator=g, device=DEV), torch.arange(t - 70, t, device=DEV)])
+    rows, some = f64(x[0, at]), lab[0, at].cpu().numpy()
+    lse = np.log(np.exp(rows).sum(-1))
+    on = some != IGNORE
+    within(f64(r.lse[0, at]), np.where(on, lse, 0.0), 40 * U * (1 + np.abs(lse)))
+    check_gradient(d[0, at], x[0, at], some, r.lse[0, at], f64(r.slope[0, at]), "bf16")
+    assert not r.slope[0, ::7].any() and bool(r.slope[0, 1::7].ne(0).any())
