@@ -11,6 +11,7 @@
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
 #include <c10/core/DeviceGuard.h>
 
+#include <initializer_list>
 #include <optional>
 #include <tuple>
 #include <vector>
@@ -73,38 +74,50 @@ void written(const Opt& t) {
 
 Tensor new_f32(at::IntArrayRef shape, const Tensor& like) { return at::empty(shape, like.options().dtype(at::kFloat)); }
 
-// Several small arrays of one call in one allocation: each an allocation of its
-// own costs the host 0.8 us, one of 13 us in a loss step of a few kilobytes.
-struct Block {
-  Tensor t;
+// The float32 arrays that a call returns.  Each has its own memory, so that one
+// that is kept holds no other; but those that fit it together share one block of
+// 512 bytes, the smallest that torch's allocator hands out (an allocation costs
+// the host 0.8 us, one of 13 us in a loss step of a few kilobytes).
+struct Results {
+  static constexpr int64_t kShared = 128;  // floats
+  const Tensor& like;
+  Tensor block;
   int64_t used = 0;
-  Block(const Tensor& like, int64_t floats) : t(at::empty({floats}, like.options().dtype(at::kFloat))) {}
-  // the next array: a tensor on the block's storage
+  // `sizes`: of the arrays, in the order in which next() makes them
+  Results(const Tensor& l, std::initializer_list<int64_t> sizes) : like(l) {
+    int64_t n = 0;
+    for (int64_t s : sizes)
+      if (n + s <= kShared) n += s;
+    if (n > 0) block = new_f32({n}, like);
+  }
   Tensor next(at::IntArrayRef shape) {
-    auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
-    impl->set_storage_offset(t.storage_offset() + used);
+    const int64_t n = c10::multiply_integers(shape);
+    if (!block.defined() || used + n > kShared) return new_f32(shape, like);
+    auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(block.storage()), block.key_set(), block.dtype());
+    impl->set_storage_offset(block.storage_offset() + used);
     impl->set_sizes_contiguous(shape);
-    used += impl->numel();
+    used += n;
     return Tensor(std::move(impl));
   }
 };
 
-// the caller's workspace or a new one
+// the caller's workspace, or new memory of the current stream's: no tensor is
+// made of it
 struct Workspace {
-  Tensor t;
-  Workspace(const Tensor& like, int64_t bytes, const Opt& given) {
+  Opt given;
+  c10::DataPtr made;
+  int64_t size;
+  Workspace(const Tensor& like, int64_t bytes, const Opt& ws) : given(ws), size(bytes) {
     if (given) {
       CHECK_VALUE(given->device() == like.device() && given->is_contiguous(),
                   "ws must be contiguous and on the tensors' device");
-      t = *given;
+      size = given->numel() * given->element_size();
     } else {
-      t = at::empty({bytes}, like.options().dtype(at::kByte));
+      made = c10::GetAllocator(like.device().type())->allocate(static_cast<size_t>(bytes));
     }
   }
-  // the first `need` bytes of a block, whose arrays follow
-  Workspace(Block& block, int64_t need) : t(block.next({need / 4})) {}
-  void* p() const { return t.data_ptr(); }
-  int64_t bytes() const { return t.numel() * t.element_size(); }
+  void* p() const { return given ? given->data_ptr() : made.get(); }
+  int64_t bytes() const { return size; }
 };
 
 // ---- layer normalisation --------------------------------------------------
@@ -147,8 +160,8 @@ std::tuple<Tensor, Tensor, Tensor> layer_norm_fwd_(const Tensor& x, const Opt& w
   const c10::DeviceGuard guard(x.device());
   Tensor out = y ? *y : at::empty(x.sizes(), x.options());
   const auto lead = x.sizes().slice(0, x.dim() - 1);
-  Block block(x, 2 * r.rows);
-  Tensor mean = block.next(lead), rstd = block.next(lead);
+  Results res(x, {r.rows, r.rows});
+  Tensor mean = res.next(lead), rstd = res.next(lead);
   check("layer_norm_fwd",
         layer_norm_fwd(x.data_ptr(), w, b, out.data_ptr(), static_cast<float*>(mean.data_ptr()),
                        static_cast<float*>(rstd.data_ptr()), r.rows, r.d, r.stride, ys, eps, code, stream_of(x)));
@@ -220,32 +233,22 @@ Tensor dlogits_of(const Tensor& logits, const Opt& out) {
 }
 finetune_dlogits dlogits_args(const Tensor& out) { return {out.data_ptr(), out.stride(0), out.stride(1)}; }
 
-// the workspace and `floats` of outputs behind it in one block, or the caller's workspace
-struct LogitsBlock {
-  Block block;
-  Workspace work;
-  LogitsBlock(const Tensor& logits, const finetune_logits& in, int64_t floats, const Opt& ws)
-      : LogitsBlock(logits, ws ? 0 : need_of(in), floats, ws) {}
-  Tensor next(at::IntArrayRef shape) { return block.next(shape); }
-
- private:
-  LogitsBlock(const Tensor& logits, int64_t need, int64_t floats, const Opt& ws)
-      : block(logits, need / 4 + floats), work(ws ? Workspace(logits, 0, ws) : Workspace(block, need)) {}
-  static int64_t need_of(const finetune_logits& in) {
-    int64_t need = 0;
-    check("finetune_logits_workspace", finetune_logits_workspace(&in, &need));
-    return need;
-  }
-};
+// the caller's workspace or a new one of the size the call needs
+Workspace logits_workspace(const Tensor& logits, const finetune_logits& in, const Opt& ws) {
+  int64_t need = 0;
+  if (!ws) check("finetune_logits_workspace", finetune_logits_workspace(&in, &need));
+  return Workspace(logits, need, ws);
+}
 
 float* ptr(const Tensor& t) { return static_cast<float*>(t.data_ptr()); }
 
 std::tuple<Tensor, Tensor> token_logprob_(const Tensor& logits, const Tensor& labels, const Opt& ws) {
   const finetune_logits in = logits_of(logits, labels);
   const c10::DeviceGuard guard(logits.device());
-  LogitsBlock block(logits, in, 2 * in.seqs * in.positions, ws);
-  const Workspace& work = block.work;
-  Tensor logp = block.next(labels.sizes()), lse = block.next(labels.sizes());
+  const Workspace work = logits_workspace(logits, in, ws);
+  const int64_t rows = labels.numel();
+  Results res(logits, {rows, rows});
+  Tensor logp = res.next(labels.sizes()), lse = res.next(labels.sizes());
   check("token_logprob", token_logprob(&in, ptr(logp), ptr(lse), work.p(), work.bytes(), stream_of(logits)));
   return {logp, lse};
 }
@@ -272,10 +275,11 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor, Opt> preference_loss_(
   const float* ref = f32("ref_logp", ref_logp, labels.sizes(), logits);
   check_dlogits(logits, dlogits);
   const c10::DeviceGuard guard(logits.device());
-  LogitsBlock block(logits, in, in.seqs / 2 + 2 * in.seqs + 2 * in.seqs * in.positions, ws);
-  const Workspace& work = block.work;
-  Tensor loss = block.next({in.seqs / 2}), ratio = block.next({in.seqs}), logp = block.next(labels.sizes()),
-         lse = block.next(labels.sizes()), slope = block.next({in.seqs});
+  const Workspace work = logits_workspace(logits, in, ws);
+  const int64_t rows = labels.numel();
+  Results res(logits, {in.seqs / 2, in.seqs, in.seqs, rows, rows});
+  Tensor loss = res.next({in.seqs / 2}), ratio = res.next({in.seqs}), slope = res.next({in.seqs}),
+         logp = res.next(labels.sizes()), lse = res.next(labels.sizes());
   const finetune_preference how{kind, average, beta, smoothing};
   if (!scale) {
     check("preference_loss_fwd", preference_loss_fwd(&in, ref, &how, ptr(loss), ptr(ratio), ptr(logp), ptr(lse),
@@ -320,10 +324,11 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor, Opt> policy_loss_(
   const float* adv = f32("advantages", advantages, advantages.sizes(), logits);
   check_dlogits(logits, dlogits);
   const c10::DeviceGuard guard(logits.device());
-  LogitsBlock block(logits, in, 2 + 3 * in.seqs * in.positions, ws);
-  const Workspace& work = block.work;
-  Tensor loss = block.next({}), kl = block.next({}), logp = block.next(labels.sizes()),
-         lse = block.next(labels.sizes()), slope = block.next(labels.sizes());
+  const Workspace work = logits_workspace(logits, in, ws);
+  const int64_t rows = labels.numel();
+  Results res(logits, {1, 1, rows, rows, rows});
+  Tensor loss = res.next({}), kl = res.next({}),  // next to each other: the call's stats
+      logp = res.next(labels.sizes()), lse = res.next(labels.sizes()), slope = res.next(labels.sizes());
   const finetune_policy how{reduction, per_token, clip_low, clip_high, kl_coef};
   if (!scale) {
     check("policy_loss_fwd", policy_loss_fwd(&in, old, ref, adv, &how, ptr(loss), ptr(logp), ptr(lse), ptr(slope),
