@@ -4,10 +4,11 @@
 
 Steps: generate csrc/twiddles.inc from float64 math, then one hipcc call each
 for librdfft.so, libfinetune.so (csrc/finetune: the operators of a fine-tuning
-step around the layers, with one g++ call for the Python module on it) and
-libstreamprobe.so (the in-place streaming pass
+step around the layers) and libstreamprobe.so (the in-place streaming pass
 that bench.py measures the transforms against).  Packed FP32 instructions are
-disabled for all device code.
+disabled for all device code.  Last comes the Python module on libfinetune.so,
+the one part that needs torch and a C++ compiler: without them the libraries
+are built all the same, and the module's calls say what is missing.
 
 kernel_resources() reads back, from the built library's own gfx950 code
 object, the register and scratch figures the compiler recorded for every
@@ -17,6 +18,7 @@ kernel (the AMDGPU code-object metadata note).
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 import tempfile
@@ -61,13 +63,14 @@ def build(verbose: bool = True) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
-    build_finetune(verbose)
+    build_finetune(verbose, host=False)
     tmp = PROBE_LIB + ".tmp"
     cmd = [HIPCC, *HIP_FLAGS, os.path.join(CSRC, "stream_probe.hip"), "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, PROBE_LIB)
+    build_host(verbose)
     return LIB
 
 
@@ -83,22 +86,38 @@ def build_finetune(verbose: bool = True, host: bool = True) -> str:
     subprocess.run(cmd, check=True)
     os.replace(tmp, FINETUNE_LIB)
     if host:
-        import sysconfig
-
-        from torch.utils import cpp_extension
-
-        includes = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include"), *cpp_extension.include_paths("cuda")]
-        tmp = FINETUNE_HOST + ".tmp"
-        cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-               "-D__HIP_PLATFORM_AMD__=1",
-               "-DTORCH_EXTENSION_NAME=_finetune_host", *[f for i in includes for f in ("-isystem", i)],
-               os.path.join(src, "finetune_host.cpp"), "-o", tmp, "-L", LIBDIR, "-lfinetune", "-Wl,-rpath,$ORIGIN",
-               *[f for i in cpp_extension.library_paths() for f in ("-L", i)], "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
-        os.replace(tmp, FINETUNE_HOST)
+        build_host(verbose)
     return FINETUNE_LIB
+
+
+def build_host(verbose: bool = True) -> str | None:
+    """The Python module on libfinetune.so; None, and no module, where torch or
+    the C++ compiler is not there."""
+    import sysconfig
+
+    try:
+        from torch.utils import cpp_extension
+    except ImportError:
+        cpp_extension = None
+    if cpp_extension is None or shutil.which(CXX) is None:
+        print(f"{os.path.basename(FINETUNE_HOST)} not built: "
+              + ("torch is not installed" if cpp_extension is None else f"no compiler {CXX}"), flush=True)
+        if os.path.exists(FINETUNE_HOST):  # of an earlier library
+            os.remove(FINETUNE_HOST)
+        return None
+    includes = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include"), *cpp_extension.include_paths("cuda")]
+    tmp = FINETUNE_HOST + ".tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D__HIP_PLATFORM_AMD__=1",
+           "-DTORCH_EXTENSION_NAME=_finetune_host", *[f for i in includes for f in ("-isystem", i)],
+           os.path.join(CSRC, "finetune", "finetune_host.cpp"), "-o", tmp, "-L", LIBDIR, "-lfinetune",
+           "-Wl,-rpath,$ORIGIN", *[f for i in cpp_extension.library_paths() for f in ("-L", i)], "-lc10", "-lc10_hip",
+           "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, FINETUNE_HOST)
+    return FINETUNE_HOST
 
 
 def kernel_resources(lib: str = LIB) -> dict:
