@@ -36,7 +36,12 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // norm of rows of 4096 bf16: forward of 16384 rows (268 MB) 52 us past the
 // caches, 48 through them, of 32768 rows 101 and 107; backward of 8192 rows
 // (201 MB) 43 and 43, of 16384 rows (403 MB) 76 and 79.
-constexpr bool past_caches(int64_t bytes) { return bytes > int64_t(320) << 20; }
+// (This size and the numbers of workgroups below are smaller in a host build
+// that runs the kernels on CPU threads.)
+#ifndef FINETUNE_CACHE_BYTES
+#define FINETUNE_CACHE_BYTES (int64_t(320) << 20)
+#endif
+constexpr bool past_caches(int64_t bytes) { return bytes > FINETUNE_CACHE_BYTES; }
 template <class F>
 void by_stream(bool stream, F f) {
   if (stream)
@@ -84,6 +89,10 @@ void by_norm_row(int64_t d, F f) {
 // sum: rows of 4096 bf16, 256 / 512 / 1024 workgroups: 2048 rows 20 / 25 / 36 us,
 // 16384 rows 80 / 86 / 102 us.  Rows of up to 1024 elements have slices small
 // enough for two a unit (32768 rows of 512: 30 / 25.5 / 27 us).
+#ifndef FINETUNE_NORM_GROUPS
+#define FINETUNE_NORM_GROUPS 256  // one a compute unit
+#endif
+constexpr int64_t kNormGroups = FINETUNE_NORM_GROUPS;
 struct DwSplit {
   int64_t parts, per;
 };
@@ -91,7 +100,7 @@ DwSplit dw_split(int64_t rows, int64_t d) {
   const int t = norm_threads(d);
   if (t) {
     const int64_t groups = ceil_div(std::max<int64_t>(rows, 1), norm_wg(t) / t);
-    return {std::min<int64_t>(groups, t >= kNormThreads ? 256 : 512), 0};
+    return {std::min<int64_t>(groups, t >= kNormThreads ? kNormGroups : 2 * kNormGroups), 0};
   }
   const int64_t cols = ceil_div(d, kNormThreads);
   const int64_t parts = std::max<int64_t>(std::min<int64_t>(1024 / cols, ceil_div(rows, 16)), 1);
@@ -114,7 +123,7 @@ int launch_norm_fwd(const void* x, const float* w, const float* b, void* y, floa
   by_norm_row<Io>(d, [&](auto t, auto ragged) {
     constexpr int TT = decltype(t)::value, WG = norm_wg(TT);
     const int64_t groups = ceil_div(rows, WG / TT);
-    const int64_t grid = std::min<int64_t>(groups, 2048 * kNormThreads / WG);
+    const int64_t grid = std::min<int64_t>(groups, 8 * kNormGroups * kNormThreads / WG);  // 32 waves a compute unit
     by_stream(past_caches(2 * rows * d * int64_t(sizeof(T))), [&](auto stream) {
       hipLaunchKernelGGL((layer_norm_fwd_kernel<Io, TT, decltype(ragged)::value, decltype(stream)::value>),
                          dim3(static_cast<unsigned>(grid)), dim3(WG), 0, s, px, w, b, py, mean, rstd, rows, n, xs, ys,
@@ -179,7 +188,6 @@ Rows<Io> rows_of(const finetune_dlogits* out) {
 // piece a thread.  (With 1024 as the limit, 999 rows of 10007 fp32 took 15.1 us
 // in two parts each and their joins, 13.4 us whole; a step of 512 rows of 50001
 // bf16 31 us in parts, 27 us with the rows held.)
-// (A host build that runs the kernels on CPU threads wants fewer.)
 #ifndef FINETUNE_WANT_GROUPS
 #define FINETUNE_WANT_GROUPS 512
 #endif
