@@ -233,8 +233,10 @@ __global__ void __launch_bounds__(kLogitThreads)
 // log2(e) cost 2.5 |x - lse| units of 2^-24 whatever offset the row has, and a
 // row of any finite values has a finite gradient.  (One multiply-add instead, x
 // log2(e) against a rounded lse log2(e) with the rest in g's factor, saves an
-// instruction an element but takes its error from x: 1.3e-4 of every softmax
-// value at logits near 1e4, NaN past 1e10.)
+// instruction an element, which shows where a row's exponentials are not hidden
+// behind its bytes: a policy step of 16384 rows of 8000 fp16 118 us, 122 us so,
+// of 8192 rows of 131072 bf16 658 us both.  But it takes its error from x: 1.3e-4
+// of every softmax value at logits near 1e4, NaN past 1e10.)
 struct RowGrad {
   float g, lse;
   int label;
