@@ -20,7 +20,7 @@ def _build(kind):
     if os.path.exists(exe) and os.path.getmtime(exe) >= max(os.path.getmtime(s) for s in [src, *build_emu.sources()]):
         return exe
     os.makedirs(build_emu.BUILD, exist_ok=True)
-    subprocess.run([build_emu.CXX, "-std=c++20", *build_emu.FLAGS[kind], "-Wno-pass-failed", "-I", build_emu.HERE, "-I",
+    subprocess.run([build_emu.CXX, "-std=c++20", *build_emu.FLAGS[kind], "-O0", "-Wno-pass-failed", "-I", build_emu.HERE, "-I",
                     os.path.join(build_emu.ROOT, "include"), "-I", build_emu.CSRC, src, "-o", exe + ".tmp", "-lpthread"],
                    check=True, capture_output=True, text=True)
     os.replace(exe + ".tmp", exe)
@@ -34,7 +34,7 @@ def _run(kind):
 
 @pytest.fixture(scope="module")
 def runs():
-    with ThreadPoolExecutor() as pool:  # each mostly the compiler's time
+    with ThreadPoolExecutor() as pool:
         return dict(zip(build_emu.FLAGS, pool.map(_run, build_emu.FLAGS)))
 
 
