@@ -4,7 +4,7 @@
 // row in the last one), and the forms of the losses and the clipping for large
 // buffers.
 //
-//   rounds [small]     small: what fits the thread checker's patience
+//   rounds [small]     small: what ThreadSanitizer runs within a minute
 #define FINETUNE_NORM_GROUPS 1     // 8 workgroups of 256 threads forward, 1 or 2 backward
 #define FINETUNE_CACHE_BYTES 8192  // of a call's large buffers
 
@@ -17,7 +17,7 @@ int main(int argc, char** argv) {
   for (int dt = 0; dt < 3; ++dt) {
     if (small && dt == 2) continue;
     layer_norm_case(560, 5, dt, 1, 1, false);  // 8 threads a row, 32 rows a workgroup: 18 groups of rows, the last half empty
-    layer_norm_case(17, 1999, dt, 1, 1, false);  // 128: two waves a row, two rows a workgroup, the last round's second missing
+    layer_norm_case(17, 1999, dt, 1, 1, false);  // 128: two waves a row, two rows a workgroup, the last pair without its second
     if (small && dt != 1) continue;
     layer_norm_case(300, 128, dt, 0, 0, true);  // ... whole pieces
     layer_norm_case(150, 250, dt, 3, 1, true);  // 16
