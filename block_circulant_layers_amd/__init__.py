@@ -4,7 +4,9 @@ The compute path is the HIP library ``lib/librdfft.so`` (C ABI in
 ``include/rdfft.h``); :mod:`block_circulant_layers_amd.binding` is its thin
 Python binding.  The operators of a fine-tuning step around the layers are in
 ``lib/libfinetune.so`` (C ABI in ``include/finetune.h``) and
-:mod:`block_circulant_layers_amd.finetune`.  Build both with
+:mod:`block_circulant_layers_amd.finetune`; those of a transformer sublayer
+(attention, relative position bias, dropout; C ABI in ``include/attention.h``) are in
+the same library and :mod:`block_circulant_layers_amd.attention`.  Build both with
 ``python -m block_circulant_layers_amd.build``.
 """
 
@@ -57,4 +59,17 @@ from .finetune import (  # noqa: F401
     token_logp,
     token_logprob,
     token_logprob_bwd,
+)
+from .attention import (  # noqa: F401
+    Dropout,
+    RelativeBias,
+    attention,
+    attention_bwd,
+    attention_fwd,
+    dropout,
+    dropout_bwd,
+    dropout_fwd,
+    relative_bias,
+    relative_bias_bwd,
+    relative_bias_fwd,
 )

@@ -4,7 +4,7 @@
 
 Steps: generate csrc/twiddles.inc from float64 math, then one hipcc call each
 for librdfft.so, libfinetune.so (csrc/finetune: the operators of a fine-tuning
-step around the layers) and libstreamprobe.so (the in-place streaming pass
+step around the layers, and those of a transformer sublayer) and libstreamprobe.so (the in-place streaming pass
 that bench.py measures the transforms against).  Packed FP32 instructions are
 disabled for all device code.  Last comes the Python module on libfinetune.so,
 the one part that needs torch and a C++ compiler: without them the libraries
@@ -30,6 +30,8 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "librdfft.so")
 # the operators of a fine-tuning step around the layers (include/finetune.h)
 FINETUNE_LIB = os.path.join(LIBDIR, "libfinetune.so")
+FINETUNE_SOURCES = ["finetune_lib.hip", "attention_lib.hip", "attention_f32.hip", "attention_bf16.hip",
+                    "attention_f16.hip"]
 # the Python module that calls it on torch tensors
 FINETUNE_HOST = os.path.join(LIBDIR, "_finetune_host.so")
 # the in-place streaming pass bench.py measures the transforms against
@@ -38,6 +40,7 @@ CXX = os.environ.get("CXX", "g++")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 LLVM_BIN = os.environ.get("RDFFT_LLVM_BIN", "/opt/rocm/llvm/bin")
 OFFLOAD_TARGET = "hipv4-amdgcn-amd-amdhsa--gfx950"
+BUNDLE_MAGIC = b"__CLANG_OFFLOAD_BUNDLE__"
 
 HIP_FLAGS = [
     "--offload-arch=gfx950",
@@ -80,7 +83,7 @@ def build_finetune(verbose: bool = True, host: bool = True) -> str:
     src = os.path.join(CSRC, "finetune")
     tmp = FINETUNE_LIB + ".tmp"
     cmd = [HIPCC, *HIP_FLAGS, "-Wl,-soname,libfinetune.so", "-I", os.path.join(ROOT, "include"),
-           os.path.join(src, "finetune_lib.hip"), "-o", tmp]
+           f"-parallel-jobs={len(FINETUNE_SOURCES)}", *[os.path.join(src, f) for f in FINETUNE_SOURCES], "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
@@ -110,7 +113,8 @@ def build_host(verbose: bool = True) -> str | None:
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            "-D__HIP_PLATFORM_AMD__=1",
            "-DTORCH_EXTENSION_NAME=_finetune_host", *[f for i in includes for f in ("-isystem", i)],
-           os.path.join(CSRC, "finetune", "finetune_host.cpp"), "-o", tmp, "-L", LIBDIR, "-lfinetune",
+           os.path.join(CSRC, "finetune", "finetune_host.cpp"), os.path.join(CSRC, "finetune", "attention_host.cpp"),
+           "-o", tmp, "-L", LIBDIR, "-lfinetune",
            "-Wl,-rpath,$ORIGIN", *[f for i in cpp_extension.library_paths() for f in ("-L", i)], "-lc10", "-lc10_hip",
            "-ltorch_cpu", "-ltorch_python"]
     if verbose:
@@ -124,29 +128,37 @@ def kernel_resources(lib: str = LIB) -> dict:
     """Per-kernel metadata of the gfx950 code object inside ``lib`` (a library
     built here): {mangled name: {"private_segment_fixed_size", "vgpr_count",
     "agpr_count", "sgpr_count", "vgpr_spill_count", "sgpr_spill_count",
-    "group_segment_fixed_size", "uses_dynamic_stack"}}.  The code object is
-    taken out of the library's offload bundle and its metadata note read as
-    YAML."""
+    "group_segment_fixed_size", "uses_dynamic_stack"}}.  The code objects are
+    taken out of the library's offload bundles (one a source file) and their
+    metadata notes read as YAML."""
     import yaml
 
+    notes = []
     with tempfile.TemporaryDirectory() as tmp:
         fat = os.path.join(tmp, "fatbin.bin")
         co = os.path.join(tmp, "gfx950.co")
         subprocess.run([os.path.join(LLVM_BIN, "llvm-objcopy"), f"--dump-section=.hip_fatbin={fat}", lib,
                         os.path.join(tmp, "stripped.so")], check=True, capture_output=True)
-        subprocess.run([os.path.join(LLVM_BIN, "clang-offload-bundler"), "--unbundle", "--type=o",
-                        f"--targets={OFFLOAD_TARGET}", f"--input={fat}", f"--output={co}"],
-                       check=True, capture_output=True)
-        notes = subprocess.run([os.path.join(LLVM_BIN, "llvm-readelf"), "--notes", co], check=True,
-                               capture_output=True, text=True).stdout
-    start = notes.index("---")
-    end = notes.index("\n...", start)
-    meta = yaml.safe_load(notes[start:end])
+        with open(fat, "rb") as f:
+            section = f.read()
+        at = section.find(BUNDLE_MAGIC)
+        while at >= 0:
+            after = section.find(BUNDLE_MAGIC, at + 1)
+            with open(fat, "wb") as f:
+                f.write(section[at:after if after >= 0 else len(section)])
+            subprocess.run([os.path.join(LLVM_BIN, "clang-offload-bundler"), "--unbundle", "--type=o",
+                            f"--targets={OFFLOAD_TARGET}", f"--input={fat}", f"--output={co}"],
+                           check=True, capture_output=True)
+            notes.append(subprocess.run([os.path.join(LLVM_BIN, "llvm-readelf"), "--notes", co], check=True,
+                                        capture_output=True, text=True).stdout)
+            at = after
     keys = ("private_segment_fixed_size", "vgpr_count", "agpr_count", "sgpr_count", "vgpr_spill_count",
             "sgpr_spill_count", "group_segment_fixed_size", "uses_dynamic_stack")
     out = {}
-    for k in meta["amdhsa.kernels"]:
-        out[k[".name"]] = {key: k.get("." + key) for key in keys}
+    for text in notes:
+        start = text.index("---")
+        for k in yaml.safe_load(text[start:text.index("\n...", start)])["amdhsa.kernels"]:
+            out[k[".name"]] = {key: k.get("." + key) for key in keys}
     return out
 
 

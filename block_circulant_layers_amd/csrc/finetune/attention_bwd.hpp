@@ -1,0 +1,476 @@
+// attention_bwd.hpp -- the attention's gradients from q, k, v, o, lse and dout; the probabilities are computed again.
+//
+// Two kernels, each of which owns what it sums, so that no sum goes through
+// atomics in memory and results repeat bit for bit:
+//   dq: a workgroup owns 128 queries and walks over the keys,
+//   dk and dv: a workgroup owns 128 keys of a key head and walks over the
+//   queries of every head that shares it.
+// Both compute scores and dp, so seven products in place of the five that the
+// gradients need; one kernel with dq summed by atomics would save two and lose
+// the fixed order.  The first one also forms delta, which the second reads.
+#pragma once
+
+#include "attention_fwd.hpp"
+
+namespace finetune {
+
+// fp32 operands of 128 elements: the kernel of dk and dv takes 32 queries at a time in place of 64, and loads them
+// only when it needs them, to do without registers in memory.
+template <class Io, int DP>
+constexpr bool kBwdTight = sizeof(typename Io::T) == 4 && DP > 64;
+template <class Io, int DP>
+constexpr int kBwdQueries = kBwdTight<Io, DP> ? 32 : 64;
+
+template <class Io, int DP>
+constexpr int kBwdWaves = DP > 64 ? 1 : sizeof(typename Io::T) == 4 && DP > 32 ? 1 : 2;
+
+// What the two kernels hand on, and the sums of split work (splits > 1).
+struct BwdParts {
+  float* delta;   // [batch, heads, queries]
+  float* peak;    // [batch, heads, queries]: the largest |dout| of a query (fp16 only)
+  float* dq;      // [q_splits, batch, heads, queries, d]
+  float* ddelta;  // [q_splits, batch, heads, queries]: parts of delta (with a bias)
+  float *dk, *dv; // [k_splits, batch, kv_heads, keys, d]
+  float* dbias;   // [buckets, heads, batch * key tiles * k_splits], or NULL
+  int q_splits, k_splits;
+};
+
+// fp16: ds is formed times a power of two that brings the largest |dout| near 1, so that small gradients keep their
+// bits and large ones do not overflow; 2^-floor(log2 peak), 1 for a row of zeros.
+__device__ __forceinline__ float inverse_power(float peak) {
+  const uint32_t e = __builtin_bit_cast(uint32_t, peak) >> 23 & 255;
+  return e == 0 || e > 250 ? 1.0f : __builtin_bit_cast(float, (254 - e) << 23);
+}
+
+template <class Io, int DP, bool BIAS>
+__global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_dq_kernel(
+    Problem a, View q, View k, View v, View o, View dout, const float* lse, View dq, BwdParts parts,
+    Buckets buckets) {
+  using T = typename Io::T;
+  using M = Mma<Io>;
+  using L = Tile<Io, DP>;
+  constexpr bool kScaled = std::is_same_v<Io, F16>;
+  constexpr int DC = DP / 16, DB = DP / 32, KB = kAttnKeys / 32;
+  extern __shared__ float attention_lds[];
+  T* sk = reinterpret_cast<T*>(attention_lds);
+  T* sv = sk + L::bytes(kAttnKeys) / sizeof(T);
+  float* line = reinterpret_cast<float*>(sv + L::bytes(kAttnKeys) / sizeof(T));
+
+  const int tiles = (a.tq + kAttnRows - 1) / kAttnRows;
+  int64_t unit, item;
+  locate(blockIdx.x, int64_t(a.batch) * a.kv_heads, int64_t(a.group) * tiles * parts.q_splits, unit, item);
+  const int b = static_cast<int>(unit / a.kv_heads), kvh = static_cast<int>(unit % a.kv_heads);
+  const int split = static_cast<int>(item % parts.q_splits);
+  item /= parts.q_splits;
+  const int tile = tiles - 1 - static_cast<int>(item % tiles);
+  const int h = kvh * a.group + static_cast<int>(item / tiles);
+
+  const int l = threadIdx.x % kWave, wave = threadIdx.x / kWave, g = l / 32;
+  const int w0 = tile * kAttnRows + wave * 32, i = w0 + l % 32;
+  const int off = a.tk - a.tq;
+  const int64_t at = (int64_t(b) * a.heads + h) * a.tq + i;
+  const float own_lse = i < a.tq ? lse[at] : -INFINITY;
+  const bool live = own_lse != -INFINITY;  // a query that saw no key has no gradient
+
+  int lo, hi;
+  span_of(a, b, lo, hi);
+  const auto end_of = [&](int query) { return a.causal && query + off + 1 < hi ? query + off + 1 : hi; };
+  const int hi_row = end_of(i), wave_hi = end_of(w0), wave_end = end_of(w0 + 31);
+  const int last = tile * kAttnRows + kAttnRows < a.tq ? tile * kAttnRows + kAttnRows : a.tq;
+  const int tile_hi = end_of(last - 1);
+  int k0 = lo / kAttnKeys, k1 = tile_hi > lo ? (tile_hi + kAttnKeys - 1) / kAttnKeys : k0;
+  if (parts.q_splits > 1) {
+    const int per = (k1 - k0 + parts.q_splits - 1) / parts.q_splits;
+    k0 += split * per;
+    k1 = k0 + per < k1 ? k0 + per : k1;
+  }
+
+  typename M::Frag qf[DC], df[DC];
+  const int64_t ii = i < a.tq ? i : 0;
+  const T *qrow = q.at<const T>(b, ii, h), *orow = o.at<const T>(b, ii, h), *drow = dout.at<const T>(b, ii, h);
+  float delta = 0.0f, peak = 0.0f;
+#pragma unroll
+  for (int c = 0; c < DC; ++c) {
+    qf[c] = row_frag<Io>(qrow, live, c, a.d);
+    df[c] = row_frag<Io>(drow, live, c, a.d);
+    const typename M::Frag of = row_frag<Io>(orow, live, c, a.d);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      delta = fmaf(static_cast<float>(df[c][j]), static_cast<float>(of[j]), delta);
+      if constexpr (kScaled) peak = fmaxf(peak, fabsf(static_cast<float>(df[c][j])));
+    }
+  }
+  delta = halves_sum(delta);
+  if constexpr (kScaled) peak = halves_max(peak);
+  const float power = kScaled ? inverse_power(peak) : 1.0f;
+  const float unlift = kScaled ? 0.00390625f : 1.0f;  // 2^-kLift
+  const float fs = power * unlift, delta_fs = delta * fs;
+  const float base = live ? kLift<Io> - own_lse * kLog2e : -INFINITY;  // p = 0
+
+  if constexpr (BIAS) load_bias<kAttnThreads>(line, a.table, a.heads, h, buckets);
+
+  Acc acc[DB];
+#pragma unroll
+  for (int n = 0; n < DB; ++n) acc[n] = zero_acc();
+  float along = 0.0f;  // sum of p dp
+
+  const T* kbase = k.at<const T>(b, 0, kvh);
+  const T* vbase = v.at<const T>(b, 0, kvh);
+  Stage<Io, DP, kAttnKeys, kAttnThreads> nk, nv;
+  if (k0 < k1) {
+    nk.load(kbase, k.st, int64_t(k0) * kAttnKeys, lo, hi, a.d);
+    nv.load(vbase, v.st, int64_t(k0) * kAttnKeys, lo, hi, a.d);
+  }
+  for (int t = k0; t < k1; ++t) {
+    __syncthreads();
+    nk.store(sk);
+    nv.store(sv);
+    __syncthreads();
+    if (t + 1 < k1) {
+      nk.load(kbase, k.st, int64_t(t + 1) * kAttnKeys, lo, hi, a.d);
+      nv.load(vbase, v.st, int64_t(t + 1) * kAttnKeys, lo, hi, a.d);
+    }
+#pragma unroll
+    for (int n = 0; n < KB; ++n) {
+      const int j0 = t * kAttnKeys + 32 * n;
+      if (j0 >= wave_end) continue;
+      Acc x = zero_acc(), dp = zero_acc();
+#pragma unroll
+      for (int c = 0; c < DC; ++c) {
+        x = M::mul(L::rows(sk, 32 * n, c), qf[c], x);
+        dp = M::mul(L::rows(sv, 32 * n, c), df[c], dp);
+      }
+      const float* bias = line;
+      float one = 0.0f;
+      bool near = false;
+      if constexpr (BIAS) {
+        const int rel_lo = j0 - (w0 + 31) - off, rel_hi = j0 + 31 - w0 - off;
+        near = rel_hi > -buckets.reach && rel_lo < buckets.reach;
+        if (near) bias = line + (j0 + 4 * g - i - off + buckets.reach + kEdge);
+        if (!near) one = line[rel_lo >= buckets.reach ? 2 * (buckets.reach + kEdge) : 0];
+      }
+      const bool edge = j0 < lo || j0 + 32 > wave_hi;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int up = 8 * (r / 4) + r % 4, j = j0 + up + 4 * g;
+        float e = fmaf(x[r], a.scale2, base);
+        if constexpr (BIAS) e += near ? bias[up] : one;
+        float p = exp2_of(e);
+        if (edge && (j < lo || j >= hi_row)) p = 0.0f;
+        if constexpr (BIAS) along = fmaf(p, dp[r], along);
+        x[r] = p * fmaf(dp[r], fs, -delta_fs);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const typename M::Frag s = frag_of<Io>(x, 8 * c);
+#pragma unroll
+        for (int e = 0; e < DB; ++e) acc[e] = M::mul(L::cols(sk, 32 * n + 16 * c, 32 * e), s, acc[e]);
+      }
+    }
+  }
+  if (i >= a.tq) return;
+  const float out_scale = live ? a.scale / power : 0.0f;
+  if constexpr (BIAS) {
+    // delta as the sum of p dp: o is rounded, and its error would stand in every sum over a bucket
+    along = halves_sum(along) * unlift;
+    if (!live) along = 0.0f;
+    delta = along;
+  }
+  const int64_t all = int64_t(a.batch) * a.heads * a.tq;
+  if (g == 0) {
+    if (BIAS && parts.q_splits > 1)
+      parts.ddelta[split * all + at] = delta;
+    else if (split == 0)
+      parts.delta[at] = delta;
+    if (kScaled && split == 0) parts.peak[at] = peak;
+  }
+  if (parts.q_splits > 1) {
+    float* out = parts.dq + (split * all + at) * a.d;
+#pragma unroll
+    for (int n = 0; n < DB; ++n)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4)
+        store_four<F32>(out, 32 * n + 2 * r + 4 * g, a.d, acc[n][r] * out_scale, acc[n][r + 1] * out_scale,
+                        acc[n][r + 2] * out_scale, acc[n][r + 3] * out_scale);
+    return;
+  }
+  T* out = dq.at<T>(b, i, h);
+#pragma unroll
+  for (int n = 0; n < DB; ++n)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+      store_four<Io>(out, 32 * n + 2 * r + 4 * g, a.d, acc[n][r] * out_scale, acc[n][r + 1] * out_scale,
+                     acc[n][r + 2] * out_scale, acc[n][r + 3] * out_scale);
+}
+
+// Scores are computed queries x keys here, so that a lane has all its scores of
+// one key and the probabilities are the operand of the products with dout and q.
+template <class Io, int DP, bool BIAS>
+__global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_dkv_kernel(
+    Problem a, View q, View k, View v, View dout, const float* lse, View dk, View dv, BwdParts parts,
+    Buckets buckets) {
+  using T = typename Io::T;
+  using M = Mma<Io>;
+  using L = Tile<Io, DP>;
+  constexpr bool kScaled = std::is_same_v<Io, F16>;
+  constexpr int DC = DP / 16, DB = DP / 32, QN = kBwdQueries<Io, DP>, QB = QN / 32;
+  extern __shared__ float attention_lds[];
+  T* sq = reinterpret_cast<T*>(attention_lds);
+  T* sd = sq + L::bytes(QN) / sizeof(T);
+  float* sbase = reinterpret_cast<float*>(sd + L::bytes(QN) / sizeof(T));  // kLift - lse in log2 units
+  float* sdelta = sbase + QN;
+  float* speak = sdelta + QN;
+  float* line = speak + QN;
+  const int width = BIAS ? bias_line(buckets) : 0;
+  float* hist = line + width;  // one a wave: sums of ds by relative position
+
+  const int tiles = (a.tk + kAttnRows - 1) / kAttnRows;
+  int64_t unit, item;
+  locate(blockIdx.x, int64_t(a.batch) * a.kv_heads, int64_t(tiles) * parts.k_splits, unit, item);
+  const int b = static_cast<int>(unit / a.kv_heads), kvh = static_cast<int>(unit % a.kv_heads);
+  const int split = static_cast<int>(item % parts.k_splits), tile = static_cast<int>(item / parts.k_splits);
+
+  const int l = threadIdx.x % kWave, wave = threadIdx.x / kWave, g = l / 32;
+  const int w0 = tile * kAttnRows + wave * 32, j = w0 + l % 32;
+  const int off = a.tk - a.tq;
+  int lo, hi;
+  span_of(a, b, lo, hi);
+  const bool valid = j >= lo && j < hi;
+  const bool some_invalid = w0 < lo || w0 + 32 > hi;
+
+  typename M::Frag kf[DC], vf[DC];
+  const T *krow = k.at<const T>(b, valid ? j : 0, kvh), *vrow = v.at<const T>(b, valid ? j : 0, kvh);
+#pragma unroll
+  for (int c = 0; c < DC; ++c) {
+    kf[c] = row_frag<Io>(krow, valid, c, a.d);
+    vf[c] = row_frag<Io>(vrow, valid, c, a.d);
+  }
+
+  // the tiles of queries [q0, q1) see keys of this tile; (head, tile) pairs are split over workgroups
+  const int t0 = tile * kAttnRows, t1 = t0 + kAttnRows;
+  const int nq = (a.tq + QN - 1) / QN;
+  int q0 = a.causal && t0 - off > 0 ? (t0 - off) / QN : 0;
+  if (q0 > nq || t1 <= lo || t0 >= hi) q0 = nq;
+  const int each = nq - q0;
+  int64_t s0 = 0, s1 = int64_t(each) * a.group;
+  if (parts.k_splits > 1) {
+    const int64_t per = (s1 + parts.k_splits - 1) / parts.k_splits;
+    s0 = split * per;
+    s1 = s0 + per < s1 ? s0 + per : s1;
+  }
+
+  Acc ak[DB], av[DB];
+#pragma unroll
+  for (int n = 0; n < DB; ++n) ak[n] = zero_acc(), av[n] = zero_acc();
+  float power = 1.0f;  // fp16: what ds is formed times
+  bool first = true;
+
+  using Rows = Stage<Io, DP, QN, kAttnThreads>;
+  Rows nx, nd;
+  const bool holes = a.begin || a.end || (a.causal && off < 0);  // there may be queries that see no key
+  for (int hh = 0; hh < a.group; ++hh) {
+    const int64_t m0 = s0 - int64_t(hh) * each, m1 = s1 - int64_t(hh) * each;
+    const int qa = q0 + static_cast<int>(m0 > 0 ? m0 : 0), qb = q0 + static_cast<int>(m1 < each ? m1 : each);
+    if (!BIAS && qa >= qb) continue;
+    const int h = kvh * a.group + hh;
+    const int64_t at = (int64_t(b) * a.heads + h) * a.tq;
+    const T *qbase = q.at<const T>(b, 0, h), *dbase = dout.at<const T>(b, 0, h);
+    if constexpr (BIAS) {
+      __syncthreads();
+      load_bias<kAttnThreads>(line, a.table, a.heads, h, buckets);
+      for (int t = threadIdx.x; t < 4 * width; t += kAttnThreads) hist[t] = 0.0f;
+      __syncthreads();
+    }
+    float nlse = -INFINITY, ndelta = 0.0f, npeak = 0.0f, row_lse[Rows::N];
+    const auto fetch_dout = [&](int t) { nd.load(dbase, dout.st, int64_t(t) * QN, 0, a.tq, a.d); };
+    const auto fetch = [&](int t) {
+      const int64_t i0 = int64_t(t) * QN;
+      nx.load(qbase, q.st, i0, 0, a.tq, a.d);
+#pragma unroll
+      for (int n = 0; n < Rows::N; ++n) {
+        const int64_t i = i0 + Rows::row(n);
+        row_lse[n] = holes && i < a.tq ? lse[at + i] : 0.0f;
+      }
+      if (threadIdx.x < QN) {
+        const int64_t i = i0 + threadIdx.x;
+        nlse = i < a.tq ? lse[at + i] : -INFINITY;
+        ndelta = i < a.tq ? parts.delta[at + i] : 0.0f;
+        if constexpr (kScaled) npeak = i < a.tq ? parts.peak[at + i] : 0.0f;
+      }
+    };
+    constexpr bool kAhead = !kBwdTight<Io, DP>;
+    if (kAhead && qa < qb) fetch(qa), fetch_dout(qa);
+    for (int t = qa; t < qb; ++t) {
+      if (!kAhead) fetch(t);
+      __syncthreads();
+      const auto mend = [&](Rows& x) {  // rows of queries without a key may hold anything
+        if (!holes) return;
+#pragma unroll
+        for (int n = 0; n < Rows::N; ++n)
+          if (row_lse[n] == -INFINITY) x.r[n] = typename L::Piece{};
+      };
+      mend(nx);
+      nx.store(sq);
+      if (!kAhead) fetch_dout(t);
+      mend(nd);
+      nd.store(sd);
+      if (threadIdx.x < QN) {
+        sbase[threadIdx.x] = nlse == -INFINITY ? -INFINITY : kLift<Io> - nlse * kLog2e;  // no keys: p = 0
+        sdelta[threadIdx.x] = ndelta;
+        if constexpr (kScaled) speak[threadIdx.x] = npeak;
+      }
+      __syncthreads();
+      if (kAhead && t + 1 < qb) fetch(t + 1), fetch_dout(t + 1);
+      const int i0 = t * QN;
+      if constexpr (kScaled) {
+        // one power of two for all of dk's sums: when a tile asks for a smaller one, the sums follow
+        const float most = lanes_reduce<kWave>(speak[l % QN], [](float x, float y) { return fmaxf(x, y); });
+        const float want = inverse_power(most);
+        if (most > 0.0f && (first || want < power)) {
+          const float ratio = want / power;
+          if (!first)
+#pragma unroll
+            for (int n = 0; n < DB; ++n)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) ak[n][r] *= ratio;
+          power = want;
+          first = false;
+        }
+      }
+      const float unlift = kScaled ? 0.00390625f : 1.0f;
+      const float fs = power * unlift;
+#pragma unroll
+      for (int n = 0; n < QB; ++n) {
+        const int r0 = i0 + 32 * n;
+        if (a.causal && r0 + 31 + off < w0) continue;  // no query of the block sees a key of the wave
+        Acc x = zero_acc(), dp = zero_acc();
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+          x = M::mul(L::rows(sq, 32 * n, c), kf[c], x);
+          dp = M::mul(L::rows(sd, 32 * n, c), vf[c], dp);
+          if constexpr (kBwdTight<Io, DP>) __builtin_amdgcn_sched_barrier(0);  // no operands loaded further ahead
+        }
+        const float* bias = line;
+        float one = 0.0f;
+        bool near = false, right = false;
+        const int rel_lo = w0 - (r0 + 31) - off, rel_hi = w0 + 31 - r0 - off;
+        const int place = w0 - r0 - off + buckets.reach + kEdge + static_cast<int>(threadIdx.x % 32) -
+                          4 * static_cast<int>(threadIdx.x % kWave / 32);  // of the lane's first query
+        if constexpr (BIAS) {
+          near = rel_hi > -buckets.reach && rel_lo < buckets.reach;
+          right = rel_lo >= buckets.reach;
+          if (near) bias = line + place;
+          if (!near) one = line[right ? 2 * (buckets.reach + kEdge) : 0];
+        }
+        const bool edge = some_invalid || (a.causal && r0 + off < w0 + 31);
+        Acc ds;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int up = 8 * (r / 4) + r % 4, row = 32 * n + up + 4 * g;
+          float e = fmaf(x[r], a.scale2, sbase[row]);
+          if constexpr (BIAS) e += near ? bias[-up] : one;
+          float p = exp2_of(e);
+          if (edge && (!valid || (a.causal && j > i0 + row + off))) p = 0.0f;
+          x[r] = p;
+          ds[r] = p * ((dp[r] - sdelta[row]) * fs);
+        }
+        if constexpr (kBwdTight<Io, DP>) __builtin_amdgcn_sched_barrier(0);
+        if constexpr (BIAS) {
+          const float undo = 1.0f / power;
+          if (near) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              __hip_atomic_fetch_add(&hist[wave * width + place - (8 * (r / 4) + r % 4)], ds[r] * undo,
+                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+          } else {  // one bucket
+            float s = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s += ds[r];
+            s = lanes_sum<kWave>(s * undo);
+            float* one_place = hist + wave * width + (right ? width - 1 : 0);
+            if (threadIdx.x % kWave == 0) *one_place += s;
+          }
+        }
+        if constexpr (kBwdTight<Io, DP>) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const typename M::Frag p = frag_of<Io>(x, 8 * c), s = frag_of<Io>(ds, 8 * c);
+#pragma unroll
+          for (int e = 0; e < DB; ++e) {
+            av[e] = M::mul(L::cols(sd, 32 * n + 16 * c, 32 * e), p, av[e]);
+            ak[e] = M::mul(L::cols(sq, 32 * n + 16 * c, 32 * e), s, ak[e]);
+            if constexpr (kBwdTight<Io, DP>) __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      }
+    }
+    if constexpr (BIAS) {
+      __syncthreads();
+      if (parts.dbias) {
+        const int64_t n = int64_t(a.batch) * tiles * parts.k_splits;
+        const int64_t mine = (int64_t(b) * tiles + tile) * parts.k_splits + split;
+        for (int c = threadIdx.x; c < buckets.count; c += kAttnThreads) {
+          int from, to;
+          buckets.range(c, buckets.reach + kEdge, from, to);
+          double s = 0.0;
+          for (int x = from; x <= to; ++x)
+            for (int w = 0; w < 4; ++w) s += hist[w * width + x + buckets.reach + kEdge];
+          parts.dbias[(int64_t(c) * a.heads + h) * n + mine] = static_cast<float>(s);
+        }
+      }
+    }
+  }
+  if (j >= a.tk) return;
+  const float down = kScaled ? 0.00390625f : 1.0f;
+  const float sk = valid ? a.scale / power : 0.0f, sv = valid ? down : 0.0f;
+  const auto value = [&](float x, float s) { return valid ? x * s : 0.0f; };
+  if (parts.k_splits > 1) {
+    const int64_t place =
+        (((int64_t(split) * a.batch + b) * a.kv_heads + kvh) * a.tk + j) * a.d;
+#pragma unroll
+    for (int n = 0; n < DB; ++n)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        const int x0 = 32 * n + 2 * r + 4 * g;
+        store_four<F32>(parts.dk + place, x0, a.d, value(ak[n][r], sk), value(ak[n][r + 1], sk),
+                        value(ak[n][r + 2], sk), value(ak[n][r + 3], sk));
+        store_four<F32>(parts.dv + place, x0, a.d, value(av[n][r], sv), value(av[n][r + 1], sv),
+                        value(av[n][r + 2], sv), value(av[n][r + 3], sv));
+      }
+    return;
+  }
+  T *ok = dk.at<T>(b, j, kvh), *ov = dv.at<T>(b, j, kvh);
+#pragma unroll
+  for (int n = 0; n < DB; ++n)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      const int x0 = 32 * n + 2 * r + 4 * g;
+      store_four<Io>(ok, x0, a.d, value(ak[n][r], sk), value(ak[n][r + 1], sk), value(ak[n][r + 2], sk),
+                     value(ak[n][r + 3], sk));
+      store_four<Io>(ov, x0, a.d, value(av[n][r], sv), value(av[n][r + 1], sv), value(av[n][r + 2], sv),
+                     value(av[n][r + 3], sv));
+    }
+}
+
+// out[b, t, h, :] = the sum of its splits in order, for [splits, batch, heads, tokens, d]; one wave a row.
+// With `dparts` also delta, from its parts.
+template <class Io>
+__global__ __launch_bounds__(kWave) void attention_sum_kernel(const float* part, int splits, int64_t rows, int heads,
+                                                              int tokens, int d, View out, const float* dparts,
+                                                              float* delta) {
+  using T = typename Io::T;
+  const int64_t row = blockIdx.x, t = row % tokens, bh = row / tokens;
+  T* to = out.at<T>(bh / heads, t, bh % heads);
+  for (int x = threadIdx.x; x < d; x += kWave) {
+    float s = 0.0f;
+    for (int n = 0; n < splits; ++n) s += part[(n * rows + row) * d + x];
+    to[x] = Io::narrow(s);
+  }
+  if (dparts && threadIdx.x == 0) {
+    float s = 0.0f;
+    for (int n = 0; n < splits; ++n) s += dparts[n * rows + row];
+    delta[row] = s;
+  }
+}
+
+}  // namespace finetune
