@@ -51,7 +51,7 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
   using L = Tile<Io, DP>;
   constexpr bool kScaled = std::is_same_v<Io, F16>;
   constexpr int DC = DP / 16, DB = DP / 32, KB = kAttnKeys / 32;
-  extern __shared__ float attention_lds[];
+  FINETUNE_DYNAMIC_LDS(attention_lds);
   T* sk = reinterpret_cast<T*>(attention_lds);
   T* sv = sk + L::bytes(kAttnKeys) / sizeof(T);
   float* line = reinterpret_cast<float*>(sv + L::bytes(kAttnKeys) / sizeof(T));
@@ -214,15 +214,17 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
   using L = Tile<Io, DP>;
   constexpr bool kScaled = std::is_same_v<Io, F16>;
   constexpr int DC = DP / 16, DB = DP / 32, QN = kBwdQueries<Io, DP>, QB = QN / 32;
-  extern __shared__ float attention_lds[];
+  FINETUNE_DYNAMIC_LDS(attention_lds);
   T* sq = reinterpret_cast<T*>(attention_lds);
   T* sd = sq + L::bytes(QN) / sizeof(T);
   float* sbase = reinterpret_cast<float*>(sd + L::bytes(QN) / sizeof(T));  // kLift - lse in log2 units
   float* sdelta = sbase + QN;
   float* speak = sdelta + QN;
   float* line = speak + QN;
-  const int width = BIAS ? bias_line(buckets) : 0;
-  float* hist = line + width;  // one a wave: sums of ds by relative position
+  const Slots slots(BIAS ? buckets.reach + kEdge : 0);
+  float* sums = line + (BIAS ? bias_line(buckets) : 0);  // of ds by relative position, a wave's after another's
+  float* mine = sums + threadIdx.x / kWave * slots.size();
+  float* block = sums + 4 * slots.size() + threadIdx.x / kWave * kBlockFloats + 32;  // the wave's
 
   const int tiles = (a.tk + kAttnRows - 1) / kAttnRows;
   int64_t unit, item;
@@ -278,7 +280,7 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
     if constexpr (BIAS) {
       __syncthreads();
       load_bias<kAttnThreads>(line, a.table, a.heads, h, buckets);
-      for (int t = threadIdx.x; t < 4 * width; t += kAttnThreads) hist[t] = 0.0f;
+      for (int t = threadIdx.x; t < 4 * slots.size(); t += kAttnThreads) sums[t] = 0.0f;
       __syncthreads();
     }
     float nlse = -INFINITY, ndelta = 0.0f, npeak = 0.0f, row_lse[Rows::N];
@@ -307,7 +309,7 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
         if (!holes) return;
 #pragma unroll
         for (int n = 0; n < Rows::N; ++n)
-          if (row_lse[n] == -INFINITY) x.r[n] = typename L::Piece{};
+          if (row_lse[n] == -INFINITY) x.zeros |= 1u << n;
       };
       mend(nx);
       nx.store(sq);
@@ -378,17 +380,25 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
         if constexpr (BIAS) {
           const float undo = 1.0f / power;
           if (near) {
+            // ds through the wave's scratch: lane t sums the diagonal key - query = t - 31 of the block
+            FINETUNE_WAVE_FENCE();
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-              __hip_atomic_fetch_add(&hist[wave * width + place - (8 * (r / 4) + r % 4)], ds[r] * undo,
-                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            for (int r = 0; r < 16; ++r) block[(8 * (r / 4) + 4 * g + r % 4) * kBlockLine + l % 32] = ds[r];
+            FINETUNE_WAVE_FENCE();
+            float s = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 32; ++r) {
+              const float v = block[r * (kBlockLine + 1) + l - 31];
+              s += static_cast<unsigned>(r + l - 31) < 32u ? v : 0.0f;
+            }
+            if (l < 63) mine[slots.at(w0 - r0 - off + l - 31)] += s * undo;
           } else {  // one bucket
             float s = 0.0f;
 #pragma unroll
             for (int r = 0; r < 16; ++r) s += ds[r];
             s = lanes_sum<kWave>(s * undo);
-            float* one_place = hist + wave * width + (right ? width - 1 : 0);
-            if (threadIdx.x % kWave == 0) *one_place += s;
+            FINETUNE_WAVE_FENCE();
+            if (l == 0) mine[slots.at(right ? slots.most : -slots.most)] += s;
           }
         }
         if constexpr (kBwdTight<Io, DP>) __builtin_amdgcn_sched_barrier(0);
@@ -408,15 +418,9 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
       __syncthreads();
       if (parts.dbias) {
         const int64_t n = int64_t(a.batch) * tiles * parts.k_splits;
-        const int64_t mine = (int64_t(b) * tiles + tile) * parts.k_splits + split;
-        for (int c = threadIdx.x; c < buckets.count; c += kAttnThreads) {
-          int from, to;
-          buckets.range(c, buckets.reach + kEdge, from, to);
-          double s = 0.0;
-          for (int x = from; x <= to; ++x)
-            for (int w = 0; w < 4; ++w) s += hist[w * width + x + buckets.reach + kEdge];
-          parts.dbias[(int64_t(c) * a.heads + h) * n + mine] = static_cast<float>(s);
-        }
+        const int64_t mine_at = (int64_t(b) * tiles + tile) * parts.k_splits + split;
+        bucket_sums(sums, slots, kAttnThreads / kWave, buckets,
+                    [&](int c, float s) { parts.dbias[(int64_t(c) * a.heads + h) * n + mine_at] = s; });
       }
     }
   }

@@ -152,6 +152,30 @@ struct Tile {
   }
 };
 
+// The 16 bytes of elements c .. of a row of d elements, zeros from d on.  Where rows end inside a piece the last one is
+// loaded from the row's last 16 bytes and shifted into place, so that nothing past the row is read.
+template <class Io>
+__device__ __forceinline__ auto piece_of(const typename Io::T* row, int c, int d) {
+  using T = typename Io::T;
+  constexpr int V = Io::kVec;
+  typedef T Piece __attribute__((ext_vector_type(V)));
+  typedef unsigned __int128 Bits;
+  const auto load = [](const T* p) { return __builtin_bit_cast(Piece, *reinterpret_cast<const typename Io::Vec*>(p)); };
+  Piece v = {};
+  if (d % V == 0) {
+    v = load(row + (c < d ? c : 0));
+  } else if (d > V) {
+    const int start = c < d - V ? c : d - V, skip = c - start;
+    v = load(row + start);
+    v = __builtin_bit_cast(Piece, __builtin_bit_cast(Bits, v) >> ((skip & (V - 1)) * 8 * int(sizeof(T))));
+  } else {
+#pragma unroll
+    for (int x = 0; x < V; ++x)
+      if (c + x < d) v[x] = row[c + x];
+  }
+  return c < d ? v : Piece{};
+}
+
 // A thread's share of a tile of ROWS rows on its way from global memory to LDS,
 // held in registers in between so that the loads run under the tile before.
 // Rows outside [lo, hi) and elements from d on become zeros and are not read.
@@ -162,56 +186,54 @@ struct Stage {
   static constexpr int N = ROWS * L::kPieces / NT;
   static_assert(N * NT == ROWS * L::kPieces, "whole pieces for each thread");
   typename L::Piece r[N];
+  uint32_t zeros;  // bit n: the n-th piece is to be zeros; applied on the way to LDS, so that no load is waited for here
 
   // of the thread's n-th piece
   static __device__ __forceinline__ int row(int n) { return (threadIdx.x + n * NT) / L::kPieces; }
+  static __device__ __forceinline__ int piece(int n) { return (threadIdx.x + n * NT) % L::kPieces; }
 
   __device__ __forceinline__ void load(const T* base, int64_t stride, int64_t row0, int64_t lo, int64_t hi, int d) {
+    zeros = 0;
+    // A tile of whole rows of whole pieces is read without a test, with 32-bit offsets from its first row.
+    if (row0 >= lo && row0 + ROWS <= hi && d % L::V == 0 && stride < (int64_t(1) << 24)) {
+      const T* first = base + row0 * stride;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int p = threadIdx.x + n * NT, row = p / L::kPieces, c = (p % L::kPieces) * L::V;
-      const int64_t j = row0 + row;
-      typename L::Piece v = {};
-      if (j >= lo && j < hi && c < d) {
-        const T* from = base + j * stride + c;
-        if (c + L::V <= d) {
-          v = __builtin_bit_cast(typename L::Piece, *reinterpret_cast<const typename Io::Vec*>(from));
-        } else {
-#pragma unroll
-          for (int x = 0; x < L::V; ++x)
-            if (c + x < d) v[x] = from[x];
-        }
+      for (int n = 0; n < N; ++n) {
+        const int c = piece(n) * L::V;
+        const uint32_t at = row(n) * static_cast<uint32_t>(stride) + (c < d ? c : 0);
+        r[n] = __builtin_bit_cast(typename L::Piece, *reinterpret_cast<const typename Io::Vec*>(first + at));
+        zeros |= c < d ? 0 : 1u << n;
       }
-      r[n] = v;
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int64_t j = row0 + row(n), near = j < lo ? lo : j >= hi ? hi - 1 : j;
+        r[n] = piece_of<Io>(base + near * stride, piece(n) * L::V, d);
+        zeros |= near == j ? 0 : 1u << n;
+      }
     }
   }
   __device__ __forceinline__ void store(T* s) const {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int p = threadIdx.x + n * NT, row = p / L::kPieces, c = p % L::kPieces;
-      *reinterpret_cast<typename L::Piece*>(s + L::at(row, c)) = r[n];
-    }
+    for (int n = 0; n < N; ++n)
+      *reinterpret_cast<typename L::Piece*>(s + L::at(row(n), piece(n))) = zeros >> n & 1 ? typename L::Piece{} : r[n];
   }
 };
 
 // B operand straight from a row in global memory: elements 16 c + 8 g .. + 7, zeros from d on
 template <class Io>
 __device__ __forceinline__ typename Mma<Io>::Frag row_frag(const typename Io::T* row, bool valid, int c, int d) {
-  using T = typename Io::T;
-  typedef T Eight __attribute__((ext_vector_type(8), aligned(sizeof(T))));
-  typedef T Plain __attribute__((ext_vector_type(8)));
   const int x0 = 16 * c + 8 * (threadIdx.x % kWave / 32);
-  Plain v = {};
-  if (valid && x0 < d) {
-    if (x0 + 8 <= d) {
-      v = __builtin_bit_cast(Plain, *reinterpret_cast<const Eight*>(row + x0));
-    } else {
+  typename Mma<Io>::Frag f;
+  if constexpr (Io::kVec == 8) {
+    const auto v = piece_of<Io>(row, x0, d);
+    f = __builtin_bit_cast(typename Mma<Io>::Frag, valid ? v : decltype(v){});
+  } else {
+    const auto lo = piece_of<Io>(row, x0, d), hi = piece_of<Io>(row, x0 + 4, d);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (x0 + j < d) v[j] = row[x0 + j];
-    }
+    for (int j = 0; j < 4; ++j) f[j] = valid ? lo[j] : 0.0f, f[4 + j] = valid ? hi[j] : 0.0f;
   }
-  return __builtin_bit_cast(typename Mma<Io>::Frag, v);
+  return f;
 }
 
 // Four values of a block of D, consecutive elements x0 .. x0 + 3 of a row, rounded and stored up to d
@@ -274,6 +296,8 @@ __device__ __forceinline__ void locate(int64_t block, int64_t units, int64_t per
 // The bias of one head by relative position, times log2(e), in LDS: positions -reach - kEdge .. reach + kEdge, so
 // that a block of 32 x 32 scores that holds any position inside [-reach, reach] reads no further.
 constexpr int kEdge = 63;
+// a wave's scratch for one block of scores in fp32, its rows an odd number of banks apart, and 32 floats before them
+constexpr int kBlockLine = 33, kBlockFloats = 32 + 32 * kBlockLine;
 __host__ __device__ __forceinline__ int bias_line(const Buckets& b) { return 2 * (b.reach + kEdge) + 1; }
 template <int NT>
 __device__ __forceinline__ void load_bias(float* line, const float* table, int heads, int h, const Buckets& b) {

@@ -36,7 +36,7 @@ __global__ __launch_bounds__(kAttnThreads, (kFwdWaves<Io, DP, BIAS>)) void atten
   using M = Mma<Io>;
   using L = Tile<Io, DP>;
   constexpr int DC = DP / 16, DB = DP / 32, KB = kAttnKeys / 32;
-  extern __shared__ float attention_lds[];
+  FINETUNE_DYNAMIC_LDS(attention_lds);
   T* sk = reinterpret_cast<T*>(attention_lds);
   T* sv = sk + L::bytes(kAttnKeys) / sizeof(T);
   float* line = reinterpret_cast<float*>(sv + L::bytes(kAttnKeys) / sizeof(T));
@@ -198,29 +198,45 @@ __global__ __launch_bounds__(kAttnThreads, (kFwdWaves<Io, DP, BIAS>)) void atten
   if (g == 0) lse[at] = total == 0.0f ? -INFINITY : (top - kLift<Io> + log2f(total)) * kLn2;
 }
 
-// The parts of a row joined: one wave a row.
-template <class Io>
-__global__ __launch_bounds__(kWave) void attention_join_kernel(Problem a, View o, float* lse, FwdParts parts) {
+// The parts of a row joined: their weights first, one a lane, then the columns, two a lane, by LANES waves that
+// each sum every LANES-th part.
+constexpr int kMaxSplits = kWave;
+template <class Io, int LANES>
+__global__ __launch_bounds__(kWave* LANES) void attention_join_kernel(Problem a, View o, float* lse, FwdParts parts) {
   using T = typename Io::T;
+  __shared__ float weight[kMaxSplits], sums[LANES][2][kWave];
   const int64_t at = blockIdx.x, all = int64_t(a.batch) * a.heads * a.tq;
+  const int l = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const float* stat = parts.stats + (l < parts.splits ? l * all + at : at) * 2;
+  const float own = l < parts.splits ? stat[0] : -INFINITY;
+  const float top = lanes_reduce<kWave>(own, [](float x, float y) { return fmaxf(x, y); });
+  const float scale = exp2_of(own - (top == -INFINITY ? 0.0f : top));
+  const float total = lanes_sum<kWave>(l < parts.splits ? stat[1] * scale : 0.0f);
+  if (wave == 0) weight[l] = scale;
+  __syncthreads();
+  float x = 0.0f, y = 0.0f;
+  const float* from = parts.o + at * a.d;
+  const int64_t step = all * a.d;
+#pragma unroll 8
+  for (int s = wave; s < parts.splits; s += LANES) {
+    const float* p = from + s * step;
+    if (l < a.d) x = fmaf(p[l], weight[s], x);
+    if (l + kWave < a.d) y = fmaf(p[l + kWave], weight[s], y);
+  }
+  if constexpr (LANES > 1) {
+    sums[wave][0][l] = x;
+    sums[wave][1][l] = y;
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int n = 1; n < LANES; ++n) x += sums[n][0][l], y += sums[n][1][l];
+  }
   const int i = static_cast<int>(at % a.tq);
   const int64_t bh = at / a.tq;
-  float top = -INFINITY;
-  for (int s = 0; s < parts.splits; ++s) top = fmaxf(top, parts.stats[(s * all + at) * 2]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  float total = 0.0f;
-  for (int s = 0; s < parts.splits; ++s) {
-    const float* st = parts.stats + (s * all + at) * 2;
-    total += st[1] * exp2_of(st[0] - base);
-  }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   T* out = o.at<T>(bh / a.heads, i, bh % a.heads);
-  for (int x = threadIdx.x; x < a.d; x += kWave) {
-    float sum = 0.0f;
-    for (int s = 0; s < parts.splits; ++s)
-      sum += parts.o[(s * all + at) * a.d + x] * exp2_of(parts.stats[(s * all + at) * 2] - base);
-    out[x] = Io::narrow(sum * inv);
-  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  if (l < a.d) out[l] = Io::narrow(x * inv);
+  if (l + kWave < a.d) out[l + kWave] = Io::narrow(y * inv);
   if (threadIdx.x == 0) lse[at] = total == 0.0f ? -INFINITY : (top - kLift<Io> + log2f(total)) * kLn2;
 }
 

@@ -71,8 +71,11 @@ int launch_fwd(const FwdCall& c) {
     });
   });
   if (code != RDFFT_OK || c.plan.fwd_splits == 1) return code;
-  hipLaunchKernelGGL((attention_join_kernel<Io>), dim3(static_cast<unsigned>(rows)), dim3(kWave), 0, c.s, c.a, c.o,
-                     c.lse, c.parts);
+  const dim3 grid(static_cast<unsigned>(rows));
+  if (c.plan.fwd_splits > 8)
+    hipLaunchKernelGGL((attention_join_kernel<Io, 8>), grid, dim3(8 * kWave), 0, c.s, c.a, c.o, c.lse, c.parts);
+  else
+    hipLaunchKernelGGL((attention_join_kernel<Io, 1>), grid, dim3(kWave), 0, c.s, c.a, c.o, c.lse, c.parts);
   return launch_status();
 }
 
@@ -86,7 +89,8 @@ int launch_bwd(const BwdCall& c) {
       constexpr bool kBias = decltype(bias)::value;
       const int line = kBias ? 4 * bias_line(c.buckets) : 0;
       const int dq_lds = 2 * Tile<Io, DP>::bytes(kAttnKeys) + line;
-      const int dkv_lds = 2 * Tile<Io, DP>::bytes(kBwdQueries<Io, DP>) + 3 * 4 * kBwdQueries<Io, DP> + 5 * line;
+      const int dkv_lds = 2 * Tile<Io, DP>::bytes(kBwdQueries<Io, DP>) + 3 * 4 * kBwdQueries<Io, DP> +
+                          (kBias ? line + 4 * 4 * (kBlockFloats + Slots(c.buckets.reach + kEdge).size()) : 0);
       int code = RDFFT_OK;
       if (c.plan.dq_blocks > 0) {
         hipLaunchKernelGGL((attention_dq_kernel<Io, DP, kBias>),

@@ -81,10 +81,10 @@ int64_t pack_of(const attention_problem& a) {
   return !a.bias && a.queries < kAttnRows ? a.heads / a.kv_heads : 1;
 }
 // In how many parts a workgroup's walk over `steps` tiles is split: where there are fewer workgroups than compute
-// units, up to two a unit, with at least two tiles left to each.
+// units, up to two a unit, with at least a tile left to each.
 int64_t splits_of(int64_t blocks, int64_t steps) {
-  if (blocks <= 0 || blocks >= kUnits) return 1;
-  return std::max<int64_t>(1, std::min(2 * kUnits / blocks, steps / 2));
+  if (blocks <= 0 || 2 * blocks > kUnits) return 1;
+  return std::max<int64_t>(1, std::min(std::min(2 * kUnits / blocks, steps), int64_t(kMaxSplits)));
 }
 
 Plan plan_of(const attention_problem& a) {
@@ -176,7 +176,8 @@ int relative_bias_bwd(const void* dbias, int64_t batch_stride, int64_t head_stri
     st = by_dtype(dtype, [&](auto io) {
       using Io = decltype(io);
       hipLaunchKernelGGL((relative_bias_bwd_kernel<Io>), dim3(static_cast<unsigned>(heads * parts)),
-                         dim3(kBiasThreads), 0, s, static_cast<const typename Io::T*>(dbias), batch_stride,
+                         dim3(kBiasThreads), 4 * kBiasThreads / kWave * Slots(b.reach + Io::kVec).size(), s,
+                         static_cast<const typename Io::T*>(dbias), batch_stride,
                          head_stride, query_stride, static_cast<float*>(ws), batch, queries, keys,
                          static_cast<int>(parts), b);
       return launch_status();

@@ -21,6 +21,12 @@
 #define FINETUNE_OPAQUE(x) asm volatile("" : "+v"(x))
 #endif
 
+// Between a lane's LDS accesses and another lane's of the same wave: the
+// hardware keeps a wave's order, and the compiler must not change it.
+#ifndef FINETUNE_WAVE_FENCE
+#define FINETUNE_WAVE_FENCE() __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront")
+#endif
+
 namespace finetune {
 
 constexpr int kWave = 64;

@@ -84,46 +84,111 @@ __global__ __launch_bounds__(kBiasThreads) void relative_bias_fwd_kernel(const f
   }
 }
 
-// Partial sums of dbias by relative position: a workgroup takes `rows` rows of a
-// head's matrix over the whole batch; a thread owns columns of the rows' skewed
-// layout... one relative position a thread, cut to [-reach, reach], so that no two
-// threads add to the same place and the order is fixed.
+// A wave's sums by relative position in [-most, most], position r in slot
+// r + most, and their sums by bucket.  A wave adds to slots of its own with plain
+// reads and writes, no two lanes to one slot: LDS atomics took 177 cycles for a
+// wave's 64 and have no order.  So that lanes 8 positions apart meet different
+// banks, slot n is stored at (n % 8) * (slots / 8) + n / 8.
+struct Slots {
+  int most, eighth;
+  __host__ __device__ __forceinline__ explicit Slots(int m) : most(m), eighth((2 * m + 1 + 7) / 8) {}
+  __host__ __device__ __forceinline__ int size() const { return 8 * eighth; }
+  __device__ __forceinline__ int at(int rel) const { return (rel + most) % 8 * eighth + (rel + most) / 8; }
+};
+
+// store(bucket, sum) for every bucket of the sums of `waves` waves, kept `size()` floats apart; a wave takes every
+// waves-th bucket.  All waves have passed a barrier since the sums were written.
+template <class F>
+__device__ __forceinline__ void bucket_sums(const float* sums, const Slots& slots, int waves, const Buckets& b,
+                                            F store) {
+  const int l = threadIdx.x % kWave;
+  for (int c = threadIdx.x / kWave; c < b.count; c += waves) {
+    int from, to;
+    b.range(c, slots.most, from, to);
+    double s = 0.0;
+    for (int r = from + l; r <= to; r += kWave)
+      for (int w = 0; w < waves; ++w) s += sums[w * slots.size() + slots.at(r)];
+    s = lanes_sum<kWave>(s);
+    if (l == 0) store(c, static_cast<float>(s));
+  }
+}
+
+// Partial sums of dbias by bucket: bound by reading dbias once.  A wave takes a
+// row at a time, 16 bytes a lane, and sums it over the batch first.  Pieces that
+// lie beyond `reach` on one side have one bucket and stay in a register; the
+// others are added to the wave's slots.
 template <class Io>
 __global__ __launch_bounds__(kBiasThreads) void relative_bias_bwd_kernel(const typename Io::T* dbias, int64_t sb,
                                                                          int64_t sh, int64_t sq, float* part,
                                                                          int64_t batch, int64_t tq, int64_t tk,
                                                                          int parts, Buckets b) {
-  __shared__ float sums[kBiasThreads];
-  __shared__ double total[2 * kMaxBuckets];
-  const int h = blockIdx.x / parts, p = blockIdx.x % parts;
+  constexpr int V = Io::kVec, kWaves = kBiasThreads / kWave;
+  FINETUNE_DYNAMIC_LDS(sums);
+  const Slots slots(b.reach + V);
+  const int h = blockIdx.x / parts, p = blockIdx.x % parts, l = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int64_t rows = (tq + parts - 1) / parts, i0 = p * rows, i1 = i0 + rows < tq ? i0 + rows : tq;
-  for (int t = threadIdx.x; t < b.count; t += kBiasThreads) total[t] = 0.0;
-  const int64_t off = tk - tq;
-  // relative positions of these rows: [-(i1 - 1) - off, tk - 1 - i0 - off], a block of threads at a time
-  const int64_t lo = -(i1 - 1) - off, hi = tk - 1 - i0 - off;
-  for (int64_t r0 = lo; r0 <= hi && i1 > i0; r0 += kBiasThreads) {
-    const int64_t rel = r0 + threadIdx.x;
-    float s = 0.0f;
-    if (rel <= hi)
-      for (int64_t n = 0; n < batch; ++n)
-        for (int64_t i = i0; i < i1; ++i) {
-          const int64_t j = rel + i + off;
-          if (j >= 0 && j < tk) s += Io::widen(dbias[n * sb + h * sh + i * sq + j]);
+  for (int t = threadIdx.x; t < kWaves * slots.size(); t += kBiasThreads) sums[t] = 0.0f;
+  __syncthreads();
+  float* mine = sums + wave * slots.size();
+  float left = 0.0f, right = 0.0f;
+  for (int64_t i = i0 + wave; i < i1; i += kWaves) {
+    const typename Io::T* row = dbias + h * sh + i * sq;
+    for (int64_t j = int64_t(l) * V; j < tk; j += kWave * V) {
+      float s[V];
+#pragma unroll
+      for (int x = 0; x < V; ++x) s[x] = 0.0f;
+      if (j + V <= tk) {
+        int64_t n = 0;
+        for (; n + 4 <= batch; n += 4) {
+          typename Io::Vec v[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) v[m] = load_vec<Io>(row + (n + m) * sb + j);
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int x = 0; x < V; ++x) s[x] += Io::widen(v[m][x]);
         }
-    __syncthreads();
-    sums[threadIdx.x] = s;
-    __syncthreads();
-    for (int c = threadIdx.x; c < b.count; c += kBiasThreads) {
-      int from, to;
-      b.range(c, 1 << 30, from, to);
-      double d = 0.0;
-      for (int64_t x = from > r0 ? from : r0; x <= to && x < r0 + kBiasThreads; ++x) d += sums[x - r0];
-      total[c] += d;
+        for (; n < batch; ++n) {
+          const typename Io::Vec v = load_vec<Io>(row + n * sb + j);
+#pragma unroll
+          for (int x = 0; x < V; ++x) s[x] += Io::widen(v[x]);
+        }
+      } else {
+        for (int64_t n = 0; n < batch; ++n)
+#pragma unroll
+          for (int x = 0; x < V; ++x)
+            if (j + x < tk) s[x] += Io::widen(row[n * sb + j + x]);
+      }
+      const int64_t rel = j - i - (tk - tq);
+      if (rel <= -b.reach - (V - 1) || rel >= b.reach) {
+        float all = s[0];
+#pragma unroll
+        for (int x = 1; x < V; ++x) all += s[x];
+        if (rel < 0)
+          left += all;
+        else
+          right += all;
+      } else {
+        FINETUNE_WAVE_FENCE();
+        float old[V];
+#pragma unroll
+        for (int x = 0; x < V; ++x) old[x] = mine[slots.at(static_cast<int>(rel) + x)];
+#pragma unroll
+        for (int x = 0; x < V; ++x) mine[slots.at(static_cast<int>(rel) + x)] = old[x] + s[x];
+        FINETUNE_WAVE_FENCE();
+      }
     }
   }
+  left = lanes_sum<kWave>(left);
+  right = lanes_sum<kWave>(right);
+  FINETUNE_WAVE_FENCE();
+  if (l == 0) {
+    mine[slots.at(-slots.most)] += left;
+    mine[slots.at(slots.most)] += right;
+  }
   __syncthreads();
-  for (int c = threadIdx.x; c < b.count; c += kBiasThreads)
-    part[(int64_t(c) * (gridDim.x / parts) + h) * parts + p] = static_cast<float>(total[c]);
+  const int64_t heads = gridDim.x / parts;
+  bucket_sums(sums, slots, kWaves, b, [&](int c, float s) { part[(int64_t(c) * heads + h) * parts + p] = s; });
 }
 
 }  // namespace finetune
