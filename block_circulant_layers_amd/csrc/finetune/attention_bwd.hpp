@@ -10,6 +10,8 @@
 // the fixed order.  The first one also forms delta, which the second reads.
 #pragma once
 
+#include <limits.h>
+
 #include "attention_fwd.hpp"
 
 namespace finetune {
@@ -21,15 +23,20 @@ constexpr bool kBwdTight = sizeof(typename Io::T) == 4 && DP > 64;
 template <class Io, int DP>
 constexpr int kBwdQueries = kBwdTight<Io, DP> ? 32 : 64;
 
-template <class Io, int DP>
-constexpr int kBwdWaves = DP > 64 ? 1 : sizeof(typename Io::T) == 4 && DP > 32 ? 1 : 2;
+template <class Io, int DP, bool BIAS>
+constexpr int kDqWaves = (sizeof(typename Io::T) == 4 && DP > 32) || (BIAS && DP > 96) ? 1 : 2;
+// operands fetched ahead by the kernel of dq, of N
+template <class Io, int DP, int N>
+constexpr int kDqGroup = DP > 96 ? 0 : kAheadOf<Io, N>;
+template <class Io, int DP, bool BIAS>
+constexpr int kDkvWaves = (sizeof(typename Io::T) == 4 && DP > 32) || DP > 64 ? 1 : 2;
 
 // What the two kernels hand on, and the sums of split work (splits > 1).
 struct BwdParts {
   float* delta;   // [batch, heads, queries]
   float* peak;    // [batch, heads, queries]: the largest |dout| of a query (fp16 only)
   float* dq;      // [q_splits, batch, heads, queries, d]
-  float* ddelta;  // [q_splits, batch, heads, queries]: parts of delta (with a bias)
+  float* ddelta;  // [q_splits, batch, heads, queries]: parts of delta
   float *dk, *dv; // [k_splits, batch, kv_heads, keys, d]
   float* dbias;   // [buckets, heads, batch * key tiles * k_splits], or NULL
   int q_splits, k_splits;
@@ -43,12 +50,13 @@ __device__ __forceinline__ float inverse_power(float peak) {
 }
 
 template <class Io, int DP, bool BIAS>
-__global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_dq_kernel(
+__global__ __launch_bounds__(kAttnThreads, (kDqWaves<Io, DP, BIAS>)) void attention_dq_kernel(
     Problem a, View q, View k, View v, View o, View dout, const float* lse, View dq, BwdParts parts,
     Buckets buckets) {
   using T = typename Io::T;
   using M = Mma<Io>;
   using L = Tile<Io, DP>;
+  constexpr bool kSplit = sizeof(T) == 2;
   constexpr bool kScaled = std::is_same_v<Io, F16>;
   constexpr int DC = DP / 16, DB = DP / 32, KB = kAttnKeys / 32;
   FINETUNE_DYNAMIC_LDS(attention_lds);
@@ -57,8 +65,8 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
   float* line = reinterpret_cast<float*>(sv + L::bytes(kAttnKeys) / sizeof(T));
 
   const int tiles = (a.tq + kAttnRows - 1) / kAttnRows;
-  int64_t unit, item;
-  locate(blockIdx.x, int64_t(a.batch) * a.kv_heads, int64_t(a.group) * tiles * parts.q_splits, unit, item);
+  uint32_t unit, item;
+  locate(blockIdx.x, a.batch * a.kv_heads, a.group * tiles * parts.q_splits, unit, item);
   const int b = static_cast<int>(unit / a.kv_heads), kvh = static_cast<int>(unit % a.kv_heads);
   const int split = static_cast<int>(item % parts.q_splits);
   item /= parts.q_splits;
@@ -68,8 +76,8 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
   const int l = threadIdx.x % kWave, wave = threadIdx.x / kWave, g = l / 32;
   const int w0 = tile * kAttnRows + wave * 32, i = w0 + l % 32;
   const int off = a.tk - a.tq;
-  const int64_t at = (int64_t(b) * a.heads + h) * a.tq + i;
-  const float own_lse = i < a.tq ? lse[at] : -INFINITY;
+  const int64_t row0 = (int64_t(b) * a.heads + h) * a.tq;
+  const float own_lse = i < a.tq ? lse[row0 + i] : -INFINITY;
   const bool live = own_lse != -INFINITY;  // a query that saw no key has no gradient
 
   int lo, hi;
@@ -130,16 +138,21 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
       nk.load(kbase, k.st, int64_t(t + 1) * kAttnKeys, lo, hi, a.d);
       nv.load(vbase, v.st, int64_t(t + 1) * kAttnKeys, lo, hi, a.d);
     }
-#pragma unroll
+#pragma unroll BIAS || DP > 96 ? 1 : KB
     for (int n = 0; n < KB; ++n) {
       const int j0 = t * kAttnKeys + 32 * n;
       if (j0 >= wave_end) continue;
+      const int lane = DP > 96 ? opaque(l) : l;  // (registers)
       Acc x = zero_acc(), dp = zero_acc();
-#pragma unroll
-      for (int c = 0; c < DC; ++c) {
-        x = M::mul(L::rows(sk, 32 * n, c), qf[c], x);
-        dp = M::mul(L::rows(sv, 32 * n, c), df[c], dp);
-      }
+      fetched_ahead<Io, 2 * DC, (kDqGroup<Io, DP, 2 * DC>)>(
+          [&](int m) { return L::rows(m % 2 ? sv : sk, 32 * n, m / 2, lane); },
+          [&](int m, auto f) {
+            if (m % 2)
+              dp = M::mul(f, df[m / 2], dp);
+            else
+              x = M::mul(f, qf[m / 2], x);
+          });
+      if constexpr (DP > 96) __builtin_amdgcn_sched_barrier(0);  // (registers)
       const float* bias = line;
       float one = 0.0f;
       bool near = false;
@@ -149,38 +162,51 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
         if (near) bias = line + (j0 + 4 * g - i - off + buckets.reach + kEdge);
         if (!near) one = line[rel_lo >= buckets.reach ? 2 * (buckets.reach + kEdge) : 0];
       }
-      const bool edge = j0 < lo || j0 + 32 > wave_hi;
+      if (j0 < lo || j0 + 32 > wave_hi) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int up = 8 * (r / 4) + r % 4, j = j0 + up + 4 * g;
-        float e = fmaf(x[r], a.scale2, base);
-        if constexpr (BIAS) e += near ? bias[up] : one;
-        float p = exp2_of(e);
-        if (edge && (j < lo || j >= hi_row)) p = 0.0f;
-        if constexpr (BIAS) along = fmaf(p, dp[r], along);
-        x[r] = p * fmaf(dp[r], fs, -delta_fs);
+        for (int r = 0; r < 16; ++r) {
+          const int j = j0 + 8 * (r / 4) + r % 4 + 4 * g;
+          if (j < lo || j >= hi_row) x[r] = -INFINITY;
+        }
       }
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const typename M::Frag s = frag_of<Io>(x, 8 * c);
+      for (int r = 0; r < 16; ++r) {
+        const int up = 8 * (r / 4) + r % 4;
+        float e = fmaf(x[r], a.scale2, base);
+        if constexpr (BIAS) e += near ? bias[up] : one;
+        const float p = exp2_of(e);
+        along = fmaf(p, dp[r], along);
+        x[r] = p * fmaf(dp[r], fs, -delta_fs);
+      }
+      // ds as the sum of two numbers of the storage type: its rounding would add to dq's own as much again, and to
+      // what o's rounding leaves in delta
 #pragma unroll
-        for (int e = 0; e < DB; ++e) acc[e] = M::mul(L::cols(sk, 32 * n + 16 * c, 32 * e), s, acc[e]);
+      for (int c = 0; c < 2; ++c) {
+        const int place = DP > 96 ? opaque(l) : l;
+        const typename M::Frag s = frag_of<Io>(x, 8 * c);
+        typename M::Frag rest = {};
+        if constexpr (kSplit) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) rest[r] = M::narrow(x[8 * c + r] - static_cast<float>(s[r]));
+        }
+        fetched_ahead<Io, DB, (kDqGroup<Io, DP, DB>)>(
+            [&](int e) { return L::cols(sk, 32 * n + 16 * c, 32 * e, place); },
+            [&](int e, auto f) {
+              acc[e] = M::mul(f, s, acc[e]);
+              if constexpr (kSplit) acc[e] = M::mul(f, rest, acc[e]);
+            });
       }
     }
   }
   if (i >= a.tq) return;
   const float out_scale = live ? a.scale / power : 0.0f;
-  if constexpr (BIAS) {
-    // delta as the sum of p dp: o is rounded, and its error would stand in every sum over a bucket
-    along = halves_sum(along) * unlift;
-    if (!live) along = 0.0f;
-    delta = along;
-  }
-  const int64_t all = int64_t(a.batch) * a.heads * a.tq;
+  // The other kernel gets delta as the sum of p dp: o is rounded, and its error would stand in every sum over queries.
+  delta = live ? halves_sum(along) * unlift : 0.0f;
+  const int64_t all = int64_t(a.batch) * a.heads * a.tq, at = row0 + i;
   if (g == 0) {
-    if (BIAS && parts.q_splits > 1)
+    if (parts.q_splits > 1)
       parts.ddelta[split * all + at] = delta;
-    else if (split == 0)
+    else
       parts.delta[at] = delta;
     if (kScaled && split == 0) parts.peak[at] = peak;
   }
@@ -206,13 +232,13 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
 // Scores are computed queries x keys here, so that a lane has all its scores of
 // one key and the probabilities are the operand of the products with dout and q.
 template <class Io, int DP, bool BIAS>
-__global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_dkv_kernel(
+__global__ __launch_bounds__(kAttnThreads, (kDkvWaves<Io, DP, BIAS>)) void attention_dkv_kernel(
     Problem a, View q, View k, View v, View dout, const float* lse, View dk, View dv, BwdParts parts,
     Buckets buckets) {
   using T = typename Io::T;
   using M = Mma<Io>;
   using L = Tile<Io, DP>;
-  constexpr bool kScaled = std::is_same_v<Io, F16>;
+  constexpr bool kScaled = std::is_same_v<Io, F16>, kNarrow = sizeof(T) == 4;
   constexpr int DC = DP / 16, DB = DP / 32, QN = kBwdQueries<Io, DP>, QB = QN / 32;
   FINETUNE_DYNAMIC_LDS(attention_lds);
   T* sq = reinterpret_cast<T*>(attention_lds);
@@ -227,10 +253,13 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
   float* block = sums + 4 * slots.size() + threadIdx.x / kWave * kBlockFloats + 32;  // the wave's
 
   const int tiles = (a.tk + kAttnRows - 1) / kAttnRows;
-  int64_t unit, item;
-  locate(blockIdx.x, int64_t(a.batch) * a.kv_heads, int64_t(tiles) * parts.k_splits, unit, item);
+  uint32_t unit, item;
+  locate(blockIdx.x, a.batch * a.kv_heads, tiles * parts.k_splits, unit, item);
   const int b = static_cast<int>(unit / a.kv_heads), kvh = static_cast<int>(unit % a.kv_heads);
-  const int split = static_cast<int>(item % parts.k_splits), tile = static_cast<int>(item / parts.k_splits);
+  const int split = static_cast<int>(item % parts.k_splits), step = static_cast<int>(item / parts.k_splits);
+  // A causal mask leaves the first tiles the most queries.  Where two workgroups share a compute unit, every other
+  // round of units goes the other way, so that a long and a short one meet.
+  const int tile = kDkvWaves<Io, DP, BIAS> == 2 && (unit >> 3) & 1 ? tiles - 1 - step : step;
 
   const int l = threadIdx.x % kWave, wave = threadIdx.x / kWave, g = l / 32;
   const int w0 = tile * kAttnRows + wave * 32, j = w0 + l % 32;
@@ -290,7 +319,7 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
       nx.load(qbase, q.st, i0, 0, a.tq, a.d);
 #pragma unroll
       for (int n = 0; n < Rows::N; ++n) {
-        const int64_t i = i0 + Rows::row(n);
+        const int64_t i = i0 + Rows::row(threadIdx.x, n);
         row_lse[n] = holes && i < a.tq ? lse[at + i] : 0.0f;
       }
       if (threadIdx.x < QN) {
@@ -317,8 +346,8 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
       mend(nd);
       nd.store(sd);
       if (threadIdx.x < QN) {
-        sbase[threadIdx.x] = nlse == -INFINITY ? -INFINITY : kLift<Io> - nlse * kLog2e;  // no keys: p = 0
-        sdelta[threadIdx.x] = ndelta;
+        sbase[threadIdx.x] = nlse == -INFINITY ? -INFINITY : kLift<Io> - nlse * kLog2e;  // without a key p = 0
+        sdelta[threadIdx.x] = -ndelta;
         if constexpr (kScaled) speak[threadIdx.x] = npeak;
       }
       __syncthreads();
@@ -341,16 +370,33 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
       }
       const float unlift = kScaled ? 0.00390625f : 1.0f;
       const float fs = power * unlift;
-#pragma unroll
+#pragma unroll 1
       for (int n = 0; n < QB; ++n) {
         const int r0 = i0 + 32 * n;
         if (a.causal && r0 + 31 + off < w0) continue;  // no query of the block sees a key of the wave
-        Acc x = zero_acc(), dp = zero_acc();
+        const int lane = kNarrow ? opaque(l) : l;  // (registers)
+        Acc x = zero_acc(), dp;  // dp - delta
 #pragma unroll
-        for (int c = 0; c < DC; ++c) {
-          x = M::mul(L::rows(sq, 32 * n, c), kf[c], x);
-          dp = M::mul(L::rows(sd, 32 * n, c), vf[c], dp);
-          if constexpr (kBwdTight<Io, DP>) __builtin_amdgcn_sched_barrier(0);  // no operands loaded further ahead
+        for (int r = 0; r < 16; ++r) {
+          const int row = 32 * n + 8 * (r / 4) + 4 * g + r % 4;
+          dp[r] = sdelta[row];
+        }
+        if constexpr (kNarrow) {
+#pragma unroll
+          for (int c = 0; c < DC; ++c) {
+            x = M::mul(L::rows(sq, 32 * n, c, lane), kf[c], x);
+            dp = M::mul(L::rows(sd, 32 * n, c, lane), vf[c], dp);
+            __builtin_amdgcn_sched_barrier(0);  // no operands loaded further ahead
+          }
+        } else {
+          fetched_ahead<Io, 2 * DC, kAheadOf<Io, 2 * DC>>(
+              [&](int m) { return L::rows(m % 2 ? sd : sq, 32 * n, m / 2, lane); },
+              [&](int m, auto f) {
+                if (m % 2)
+                  dp = M::mul(f, vf[m / 2], dp);
+                else
+                  x = M::mul(f, kf[m / 2], x);
+              });
         }
         const float* bias = line;
         float one = 0.0f;
@@ -364,17 +410,21 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
           if (near) bias = line + place;
           if (!near) one = line[right ? 2 * (buckets.reach + kEdge) : 0];
         }
-        const bool edge = some_invalid || (a.causal && r0 + off < w0 + 31);
+        if (some_invalid || (a.causal && r0 + off < w0 + 31)) {
+          const int last = valid ? a.causal ? j - off : INT_MIN : INT_MAX;  // queries before it do not see the key
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (r0 + 8 * (r / 4) + r % 4 + 4 * g < last) x[r] = -INFINITY;
+        }
         Acc ds;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int up = 8 * (r / 4) + r % 4, row = 32 * n + up + 4 * g;
-          float e = fmaf(x[r], a.scale2, sbase[row]);
+          const int up = 8 * (r / 4) + r % 4;
+          float e = fmaf(x[r], a.scale2, sbase[32 * n + up + 4 * g]);
           if constexpr (BIAS) e += near ? bias[-up] : one;
-          float p = exp2_of(e);
-          if (edge && (!valid || (a.causal && j > i0 + row + off))) p = 0.0f;
+          const float p = exp2_of(e);
           x[r] = p;
-          ds[r] = p * ((dp[r] - sdelta[row]) * fs);
+          ds[r] = p * (kScaled ? dp[r] * fs : dp[r]);
         }
         if constexpr (kBwdTight<Io, DP>) __builtin_amdgcn_sched_barrier(0);
         if constexpr (BIAS) {
@@ -401,16 +451,30 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
             if (l == 0) mine[slots.at(right ? slots.most : -slots.most)] += s;
           }
         }
-        if constexpr (kBwdTight<Io, DP>) __builtin_amdgcn_sched_barrier(0);
+        if constexpr (kNarrow) {
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const typename M::Frag p = frag_of<Io>(x, 8 * c), s = frag_of<Io>(ds, 8 * c);
+          for (int c = 0; c < 2; ++c) {
+            const typename M::Frag p = frag_of<Io>(x, 8 * c), s = frag_of<Io>(ds, 8 * c);
 #pragma unroll
-          for (int e = 0; e < DB; ++e) {
-            av[e] = M::mul(L::cols(sd, 32 * n + 16 * c, 32 * e), p, av[e]);
-            ak[e] = M::mul(L::cols(sq, 32 * n + 16 * c, 32 * e), s, ak[e]);
-            if constexpr (kBwdTight<Io, DP>) __builtin_amdgcn_sched_barrier(0);
+            for (int e = 0; e < DB; ++e) {
+              av[e] = M::mul(L::cols(sd, 32 * n + 16 * c, 32 * e, lane), p, av[e]);
+              ak[e] = M::mul(L::cols(sq, 32 * n + 16 * c, 32 * e, lane), s, ak[e]);
+              __builtin_amdgcn_sched_barrier(0);
+            }
           }
+        } else {
+          const typename M::Frag p[2] = {frag_of<Io>(x, 0), frag_of<Io>(x, 8)},
+                                 s[2] = {frag_of<Io>(ds, 0), frag_of<Io>(ds, 8)};
+          fetched_ahead<Io, 4 * DB, kAheadOf<Io, 4 * DB>>(
+              [&](int m) { return L::cols(m % 2 ? sq : sd, 32 * n + 16 * (m / 2 / DB), 32 * (m / 2 % DB), lane); },
+              [&](int m, auto f) {
+                const int c = m / 2 / DB, e = m / 2 % DB;
+                if (m % 2)
+                  ak[e] = M::mul(f, s[c], ak[e]);
+                else
+                  av[e] = M::mul(f, p[c], av[e]);
+              });
         }
       }
     }
@@ -425,8 +489,7 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
     }
   }
   if (j >= a.tk) return;
-  const float down = kScaled ? 0.00390625f : 1.0f;
-  const float sk = valid ? a.scale / power : 0.0f, sv = valid ? down : 0.0f;
+  const float mk = a.scale / power, mv = kScaled ? 0.00390625f : 1.0f;
   const auto value = [&](float x, float s) { return valid ? x * s : 0.0f; };
   if (parts.k_splits > 1) {
     const int64_t place =
@@ -436,10 +499,10 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
         const int x0 = 32 * n + 2 * r + 4 * g;
-        store_four<F32>(parts.dk + place, x0, a.d, value(ak[n][r], sk), value(ak[n][r + 1], sk),
-                        value(ak[n][r + 2], sk), value(ak[n][r + 3], sk));
-        store_four<F32>(parts.dv + place, x0, a.d, value(av[n][r], sv), value(av[n][r + 1], sv),
-                        value(av[n][r + 2], sv), value(av[n][r + 3], sv));
+        store_four<F32>(parts.dk + place, x0, a.d, value(ak[n][r], mk), value(ak[n][r + 1], mk),
+                        value(ak[n][r + 2], mk), value(ak[n][r + 3], mk));
+        store_four<F32>(parts.dv + place, x0, a.d, value(av[n][r], mv), value(av[n][r + 1], mv),
+                        value(av[n][r + 2], mv), value(av[n][r + 3], mv));
       }
     return;
   }
@@ -449,10 +512,10 @@ __global__ __launch_bounds__(kAttnThreads, (kBwdWaves<Io, DP>)) void attention_d
 #pragma unroll
     for (int r = 0; r < 16; r += 4) {
       const int x0 = 32 * n + 2 * r + 4 * g;
-      store_four<Io>(ok, x0, a.d, value(ak[n][r], sk), value(ak[n][r + 1], sk), value(ak[n][r + 2], sk),
-                     value(ak[n][r + 3], sk));
-      store_four<Io>(ov, x0, a.d, value(av[n][r], sv), value(av[n][r + 1], sv), value(av[n][r + 2], sv),
-                     value(av[n][r + 3], sv));
+      store_four<Io>(ok, x0, a.d, value(ak[n][r], mk), value(ak[n][r + 1], mk), value(ak[n][r + 2], mk),
+                     value(ak[n][r + 3], mk));
+      store_four<Io>(ov, x0, a.d, value(av[n][r], mv), value(av[n][r + 1], mv), value(av[n][r + 2], mv),
+                     value(av[n][r + 3], mv));
     }
 }
 

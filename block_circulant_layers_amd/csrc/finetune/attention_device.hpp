@@ -112,9 +112,9 @@ struct Tile {
   }
   static __device__ __forceinline__ int at(int row, int piece) { return row * kStride + ((piece ^ turn(row)) * V); }
 
-  // A operand: rows r0 + l % 32, elements 16 c + 8 (l / 32) .. + 7
-  static __device__ __forceinline__ typename Mma<Io>::Frag rows(const T* s, int r0, int c) {
-    const int l = threadIdx.x % kWave, row = r0 + l % 32, g = l / 32;
+  // A operand for lane l: rows r0 + l % 32, elements 16 c + 8 (l / 32) .. + 7
+  static __device__ __forceinline__ typename Mma<Io>::Frag rows(const T* s, int r0, int c, int l) {
+    const int row = r0 + l % 32, g = l / 32;
     typename Mma<Io>::Frag f;
     if constexpr (V == 8) {
       f = __builtin_bit_cast(typename Mma<Io>::Frag, *reinterpret_cast<const Piece*>(s + at(row, 2 * c + g)));
@@ -130,8 +130,8 @@ struct Tile {
   // A operand of the transposed tile: its row l % 32 is column c0 + l % 32 here, its columns are the rows
   // r0 + {4g .. 4g + 3, 8 + 4g .. 8 + 4g + 3}.  16-bit types: the LDS's transposed reads, in which 16 lanes
   // fetch 4 rows of 16 elements and lane i gets the i-th element of each.
-  static __device__ __forceinline__ typename Mma<Io>::Frag cols(const T* s, int r0, int c0) {
-    const int l = threadIdx.x % kWave, g = l / 32;
+  static __device__ __forceinline__ typename Mma<Io>::Frag cols(const T* s, int r0, int c0, int l) {
+    const int g = l / 32;
     typename Mma<Io>::Frag f;
     if constexpr (V == 8) {
       typedef short Four __attribute__((ext_vector_type(4)));
@@ -176,6 +176,39 @@ __device__ __forceinline__ auto piece_of(const typename Io::T* row, int c, int d
   return c < d ? v : Piece{};
 }
 
+// use(i, load(i)) for i = 0 .. N - 1, the operands fetched from LDS a group of G ahead (0: as the compiler likes): an operand takes its product
+// 32 cycles and LDS some 200, and the compiler by itself fetches one ahead.
+template <class Io, int N, int G, class L, class U>
+__device__ __forceinline__ void fetched_ahead(L load, U use) {
+  static_assert(G == 0 || N % G == 0, "whole groups");
+  if constexpr (G == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) use(i, load(i));
+  }
+  typename Mma<Io>::Frag f[2][G > 0 ? G : 1];
+#pragma unroll
+  for (int i = 0; i < G; ++i) f[0][i] = load(i);
+#pragma unroll
+  for (int s = 0; s < (G > 0 ? N / G : 0); ++s) {
+    if ((s + 1) * G < N) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) f[(s + 1) % 2][i] = load((s + 1) * G + i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < G; ++i) use(s * G + i, f[s % 2][i]);
+  }
+}
+// how many operands ahead, of N: four of the 16-bit types
+template <class Io, int N>
+constexpr int kAheadOf = sizeof(typename Io::T) == 4 ? 0 : N % 4 == 0 ? 4 : N % 2 == 0 ? 2 : 0;
+
+// A lane's number that the compiler must not trace back: what is worked out from it takes no registers meanwhile.
+__device__ __forceinline__ int opaque(int l) {
+  FINETUNE_OPAQUE(l);
+  return l;
+}
+
 // A thread's share of a tile of ROWS rows on its way from global memory to LDS,
 // held in registers in between so that the loads run under the tile before.
 // Rows outside [lo, hi) and elements from d on become zeros and are not read.
@@ -188,35 +221,41 @@ struct Stage {
   typename L::Piece r[N];
   uint32_t zeros;  // bit n: the n-th piece is to be zeros; applied on the way to LDS, so that no load is waited for here
 
-  // of the thread's n-th piece
-  static __device__ __forceinline__ int row(int n) { return (threadIdx.x + n * NT) / L::kPieces; }
-  static __device__ __forceinline__ int piece(int n) { return (threadIdx.x + n * NT) % L::kPieces; }
+  // of thread t's n-th piece
+  static __device__ __forceinline__ int row(int t, int n) { return (t + n * NT) / L::kPieces; }
+  static __device__ __forceinline__ int piece(int t, int n) { return (t + n * NT) % L::kPieces; }
 
   __device__ __forceinline__ void load(const T* base, int64_t stride, int64_t row0, int64_t lo, int64_t hi, int d) {
+    const int t = opaque(threadIdx.x);
     zeros = 0;
     // A tile of whole rows of whole pieces is read without a test, with 32-bit offsets from its first row.
     if (row0 >= lo && row0 + ROWS <= hi && d % L::V == 0 && stride < (int64_t(1) << 24)) {
       const T* first = base + row0 * stride;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int c = piece(n) * L::V;
-        const uint32_t at = row(n) * static_cast<uint32_t>(stride) + (c < d ? c : 0);
+        const int c = piece(t, n) * L::V;
+        const uint32_t at = row(t, n) * static_cast<uint32_t>(stride) + (c < d ? c : 0);
         r[n] = __builtin_bit_cast(typename L::Piece, *reinterpret_cast<const typename Io::Vec*>(first + at));
         zeros |= c < d ? 0 : 1u << n;
       }
     } else {
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int64_t j = row0 + row(n), near = j < lo ? lo : j >= hi ? hi - 1 : j;
-        r[n] = piece_of<Io>(base + near * stride, piece(n) * L::V, d);
+        const int64_t j = row0 + row(t, n), near = j < lo ? lo : j >= hi ? hi - 1 : j;
+        r[n] = piece_of<Io>(base + near * stride, piece(t, n) * L::V, d);
         zeros |= near == j ? 0 : 1u << n;
       }
     }
   }
-  __device__ __forceinline__ void store(T* s) const {
+  __device__ __forceinline__ void store(T* s) {
+    const int t = opaque(threadIdx.x);
+    if (__any(zeros != 0)) {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      *reinterpret_cast<typename L::Piece*>(s + L::at(row(n), piece(n))) = zeros >> n & 1 ? typename L::Piece{} : r[n];
+      for (int n = 0; n < N; ++n)
+        if (zeros >> n & 1) r[n] = typename L::Piece{};
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) *reinterpret_cast<typename L::Piece*>(s + L::at(row(t, n), piece(t, n))) = r[n];
   }
 };
 
@@ -282,9 +321,9 @@ __device__ __forceinline__ void span_of(const Problem& a, int b, int& lo, int& h
 // (sequence, head group).  Workgroups go around the 8 XCDs in turn, so where the
 // units divide evenly each XCD gets whole units, whose keys and values then
 // come from its own L2.
-__device__ __forceinline__ void locate(int64_t block, int64_t units, int64_t per, int64_t& unit, int64_t& item) {
+__device__ __forceinline__ void locate(uint32_t block, uint32_t units, uint32_t per, uint32_t& unit, uint32_t& item) {
   if (units % 8 == 0) {
-    const int64_t n = block / 8;
+    const uint32_t n = block / 8;
     unit = n / per * 8 + block % 8;
     item = n % per;
   } else {

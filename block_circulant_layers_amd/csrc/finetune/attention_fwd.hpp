@@ -42,8 +42,8 @@ __global__ __launch_bounds__(kAttnThreads, (kFwdWaves<Io, DP, BIAS>)) void atten
   float* line = reinterpret_cast<float*>(sv + L::bytes(kAttnKeys) / sizeof(T));
 
   const int rows = a.tq * pack, tiles = (rows + kAttnRows - 1) / kAttnRows;
-  int64_t unit, item;
-  locate(blockIdx.x, int64_t(a.batch) * a.kv_heads, int64_t(a.group / pack) * tiles * parts.splits, unit, item);
+  uint32_t unit, item;
+  locate(blockIdx.x, a.batch * a.kv_heads, a.group / pack * tiles * parts.splits, unit, item);
   const int b = static_cast<int>(unit / a.kv_heads), kvh = static_cast<int>(unit % a.kv_heads);
   const int split = static_cast<int>(item % parts.splits);
   item /= parts.splits;
@@ -105,11 +105,10 @@ __global__ __launch_bounds__(kAttnThreads, (kFwdWaves<Io, DP, BIAS>)) void atten
     if (j0 >= wave_end) continue;  // none of the wave's rows sees these keys
     Acc x[KB];
 #pragma unroll
-    for (int n = 0; n < KB; ++n) {
-      x[n] = zero_acc();
-#pragma unroll
-      for (int c = 0; c < DC; ++c) x[n] = M::mul(L::rows(sk, 32 * n, c), qf[c], x[n]);
-    }
+    for (int n = 0; n < KB; ++n) x[n] = zero_acc();
+    fetched_ahead<Io, KB * DC, kAheadOf<Io, KB * DC>>(
+        [&](int m) { return L::rows(sk, 32 * (m % KB), m / KB, l); },
+        [&](int m, auto f) { x[m % KB] = M::mul(f, qf[m / KB], x[m % KB]); });
     if constexpr (BIAS) {
 #pragma unroll
       for (int n = 0; n < KB; ++n) {
@@ -161,14 +160,12 @@ __global__ __launch_bounds__(kAttnThreads, (kFwdWaves<Io, DP, BIAS>)) void atten
         for (int r = 0; r < 16; ++r) acc[n][r] *= keep;
     }
     top = m;
+    typename M::Frag p[2 * KB];
 #pragma unroll
-    for (int n = 0; n < KB; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const typename M::Frag p = frag_of<Io>(x[n], 8 * c);
-#pragma unroll
-        for (int e = 0; e < DB; ++e) acc[e] = M::mul(L::cols(sv, 32 * n + 16 * c, 32 * e), p, acc[e]);
-      }
+    for (int c = 0; c < 2 * KB; ++c) p[c] = frag_of<Io>(x[c / 2], 8 * (c % 2));
+    fetched_ahead<Io, 2 * KB * DB, kAheadOf<Io, 2 * KB * DB>>(
+        [&](int m) { return L::cols(sv, 16 * (m / DB), 32 * (m % DB), l); },
+        [&](int m, auto f) { acc[m % DB] = M::mul(f, p[m / DB], acc[m % DB]); });
   }
   total = halves_sum(total);
   if (!live) return;

@@ -100,14 +100,14 @@ int launch_bwd(const BwdCall& c) {
         if (code == RDFFT_OK && c.plan.q_splits > 1) {
           hipLaunchKernelGGL((attention_sum_kernel<Io>), dim3(static_cast<unsigned>(rows)), dim3(kWave), 0, c.s,
                              c.parts.dq, c.parts.q_splits, rows, a.heads, a.tq, a.d, c.dq,
-                             kBias ? c.parts.ddelta : nullptr, c.parts.delta);
+                             c.parts.ddelta, c.parts.delta);
           code = launch_status();
         }
       }
       if (code != RDFFT_OK || c.plan.dkv_blocks == 0) return code;
       hipLaunchKernelGGL((attention_dkv_kernel<Io, DP, kBias>),
-                         dim3(static_cast<unsigned>(c.plan.dkv_blocks * c.plan.k_splits)), dim3(kAttnThreads),
-                         dkv_lds, c.s, a, c.q, c.k, c.v, c.dout, c.lse, c.dk, c.dv, c.parts, c.buckets);
+                         dim3(static_cast<unsigned>(c.plan.dkv_blocks * c.plan.k_splits)),
+                         dim3(kAttnThreads), dkv_lds, c.s, a, c.q, c.k, c.v, c.dout, c.lse, c.dk, c.dv, c.parts, c.buckets);
       code = launch_status();
       if (code != RDFFT_OK || c.plan.k_splits == 1) return code;
       for (int n = 0; n < 2; ++n)

@@ -110,7 +110,7 @@ Plan plan_of(const attention_problem& a) {
   p.delta = take(rows);
   p.peak = take(a.dtype == RDFFT_F16 ? rows : 0);
   p.dq = take(p.q_splits > 1 ? p.q_splits * rows * a.head_dim : 0);
-  p.ddelta = take(p.q_splits > 1 && a.bias ? p.q_splits * rows : 0);
+  p.ddelta = take(p.q_splits > 1 ? p.q_splits * rows : 0);
   p.dk = take(p.k_splits > 1 ? p.k_splits * keys * a.head_dim : 0);
   p.dv = take(p.k_splits > 1 ? p.k_splits * keys * a.head_dim : 0);
   p.dbias = take(a.bias ? a.buckets.count * a.heads * a.batch * tiles * p.k_splits : 0);
