@@ -138,21 +138,19 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<Io, DP, BIAS>)) void attent
       nk.load(kbase, k.st, int64_t(t + 1) * kAttnKeys, lo, hi, a.d);
       nv.load(vbase, v.st, int64_t(t + 1) * kAttnKeys, lo, hi, a.d);
     }
-#pragma unroll BIAS || DP > 96 ? 1 : KB
+#pragma unroll BIAS ? 1 : KB
     for (int n = 0; n < KB; ++n) {
       const int j0 = t * kAttnKeys + 32 * n;
       if (j0 >= wave_end) continue;
-      const int lane = DP > 96 ? opaque(l) : l;  // (registers)
       Acc x = zero_acc(), dp = zero_acc();
       fetched_ahead<Io, 2 * DC, (kDqGroup<Io, DP, 2 * DC>)>(
-          [&](int m) { return L::rows(m % 2 ? sv : sk, 32 * n, m / 2, lane); },
+          [&](int m) { return L::rows(m % 2 ? sv : sk, 32 * n, m / 2, l); },
           [&](int m, auto f) {
             if (m % 2)
               dp = M::mul(f, df[m / 2], dp);
             else
               x = M::mul(f, qf[m / 2], x);
           });
-      if constexpr (DP > 96) __builtin_amdgcn_sched_barrier(0);  // (registers)
       const float* bias = line;
       float one = 0.0f;
       bool near = false;
@@ -182,7 +180,6 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<Io, DP, BIAS>)) void attent
       // what o's rounding leaves in delta
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int place = DP > 96 ? opaque(l) : l;
         const typename M::Frag s = frag_of<Io>(x, 8 * c);
         typename M::Frag rest = {};
         if constexpr (kSplit) {
@@ -190,7 +187,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<Io, DP, BIAS>)) void attent
           for (int r = 0; r < 8; ++r) rest[r] = M::narrow(x[8 * c + r] - static_cast<float>(s[r]));
         }
         fetched_ahead<Io, DB, (kDqGroup<Io, DP, DB>)>(
-            [&](int e) { return L::cols(sk, 32 * n + 16 * c, 32 * e, place); },
+            [&](int e) { return L::cols(sk, 32 * n + 16 * c, 32 * e, l); },
             [&](int e, auto f) {
               acc[e] = M::mul(f, s, acc[e]);
               if constexpr (kSplit) acc[e] = M::mul(f, rest, acc[e]);
@@ -198,10 +195,11 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<Io, DP, BIAS>)) void attent
       }
     }
   }
+  along = halves_sum(along);
   if (i >= a.tq) return;
   const float out_scale = live ? a.scale / power : 0.0f;
   // The other kernel gets delta as the sum of p dp: o is rounded, and its error would stand in every sum over queries.
-  delta = live ? halves_sum(along) * unlift : 0.0f;
+  delta = live ? along * unlift : 0.0f;
   const int64_t all = int64_t(a.batch) * a.heads * a.tq, at = row0 + i;
   if (g == 0) {
     if (parts.q_splits > 1)
@@ -519,21 +517,33 @@ __global__ __launch_bounds__(kAttnThreads, (kDkvWaves<Io, DP, BIAS>)) void atten
     }
 }
 
-// out[b, t, h, :] = the sum of its splits in order, for [splits, batch, heads, tokens, d]; one wave a row.
-// With `dparts` also delta, from its parts.
+// out[b, t, h, :] = the sum of its splits in order, for [splits, batch, heads, tokens, d]; one wave a row, two a lane.
+// `first` and `second` (dk and dv) in one launch, the second's rows after the first's; with `dparts` also delta, from
+// its parts.
+struct SumJob {
+  const float* part;
+  View out;
+};
 template <class Io>
-__global__ __launch_bounds__(kWave) void attention_sum_kernel(const float* part, int splits, int64_t rows, int heads,
-                                                              int tokens, int d, View out, const float* dparts,
+__global__ __launch_bounds__(kWave) void attention_sum_kernel(SumJob first, SumJob second, int splits, int64_t rows,
+                                                              int heads, int tokens, int d, const float* dparts,
                                                               float* delta) {
   using T = typename Io::T;
-  const int64_t row = blockIdx.x, t = row % tokens, bh = row / tokens;
-  T* to = out.at<T>(bh / heads, t, bh % heads);
-  for (int x = threadIdx.x; x < d; x += kWave) {
-    float s = 0.0f;
-    for (int n = 0; n < splits; ++n) s += part[(n * rows + row) * d + x];
-    to[x] = Io::narrow(s);
+  const bool other = blockIdx.x >= rows;
+  const int64_t row = other ? blockIdx.x - rows : blockIdx.x, t = row % tokens, bh = row / tokens;
+  T* to = other ? second.out.at<T>(bh / heads, t, bh % heads) : first.out.at<T>(bh / heads, t, bh % heads);
+  const float* part = (other ? second.part : first.part) + row * d;
+  const int l = threadIdx.x;
+  float x = 0.0f, y = 0.0f;
+#pragma unroll 8
+  for (int n = 0; n < splits; ++n) {
+    const float* from = part + n * rows * d;
+    if (l < d) x += from[l];
+    if (l + kWave < d) y += from[l + kWave];
   }
-  if (dparts && threadIdx.x == 0) {
+  if (l < d) to[l] = Io::narrow(x);
+  if (l + kWave < d) to[l + kWave] = Io::narrow(y);
+  if (dparts && l == 0) {
     float s = 0.0f;
     for (int n = 0; n < splits; ++n) s += dparts[n * rows + row];
     delta[row] = s;

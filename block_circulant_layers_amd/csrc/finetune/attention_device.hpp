@@ -19,6 +19,14 @@
 namespace finetune {
 
 typedef float Acc __attribute__((ext_vector_type(16)));
+typedef short ShortFour __attribute__((ext_vector_type(4)));
+
+// Four 16-bit elements by the LDS's transposed read: 16 lanes give the addresses of 4 elements each, together 4 rows
+// of 16 (lanes 4 r .. 4 r + 3 row r), and lane i gets the i-th element of each row.  A host build defines it otherwise.
+#ifndef FINETUNE_READ_TRANSPOSED
+#define FINETUNE_READ_TRANSPOSED(p) \
+  __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) finetune::ShortFour*)(p))
+#endif
 
 template <class Io>
 struct Mma;
@@ -128,20 +136,17 @@ struct Tile {
   }
 
   // A operand of the transposed tile: its row l % 32 is column c0 + l % 32 here, its columns are the rows
-  // r0 + {4g .. 4g + 3, 8 + 4g .. 8 + 4g + 3}.  16-bit types: the LDS's transposed reads, in which 16 lanes
-  // fetch 4 rows of 16 elements and lane i gets the i-th element of each.
+  // r0 + {4g .. 4g + 3, 8 + 4g .. 8 + 4g + 3}.
   static __device__ __forceinline__ typename Mma<Io>::Frag cols(const T* s, int r0, int c0, int l) {
     const int g = l / 32;
     typename Mma<Io>::Frag f;
     if constexpr (V == 8) {
-      typedef short Four __attribute__((ext_vector_type(4)));
-      typedef __attribute__((address_space(3))) Four LdsFour;
       const int col = c0 + 16 * (l % 32 / 16) + 4 * (l % 4), row = r0 + 4 * g + l % 16 / 4;
       struct {
-        Four a, b;
+        ShortFour a, b;
       } both;
-      both.a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsFour*)(s + at(row, col / 8) + col % 8));
-      both.b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsFour*)(s + at(row + 8, col / 8) + col % 8));
+      both.a = FINETUNE_READ_TRANSPOSED(s + at(row, col / 8) + col % 8);
+      both.b = FINETUNE_READ_TRANSPOSED(s + at(row + 8, col / 8) + col % 8);
       f = __builtin_bit_cast(typename Mma<Io>::Frag, both);
     } else {
       const int col = c0 + l % 32;
@@ -335,8 +340,9 @@ __device__ __forceinline__ void locate(uint32_t block, uint32_t units, uint32_t 
 // The bias of one head by relative position, times log2(e), in LDS: positions -reach - kEdge .. reach + kEdge, so
 // that a block of 32 x 32 scores that holds any position inside [-reach, reach] reads no further.
 constexpr int kEdge = 63;
-// a wave's scratch for one block of scores in fp32, its rows an odd number of banks apart, and 32 floats before them
-constexpr int kBlockLine = 33, kBlockFloats = 32 + 32 * kBlockLine;
+// a wave's scratch for one block of scores in fp32, its rows an odd number of banks apart, and 32 floats before and
+// after them, where reads along a diagonal begin and end
+constexpr int kBlockLine = 33, kBlockFloats = 64 + 32 * kBlockLine;
 __host__ __device__ __forceinline__ int bias_line(const Buckets& b) { return 2 * (b.reach + kEdge) + 1; }
 template <int NT>
 __device__ __forceinline__ void load_bias(float* line, const float* table, int heads, int h, const Buckets& b) {

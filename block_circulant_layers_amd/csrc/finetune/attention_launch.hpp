@@ -99,7 +99,7 @@ int launch_bwd(const BwdCall& c) {
         code = launch_status();
         if (code == RDFFT_OK && c.plan.q_splits > 1) {
           hipLaunchKernelGGL((attention_sum_kernel<Io>), dim3(static_cast<unsigned>(rows)), dim3(kWave), 0, c.s,
-                             c.parts.dq, c.parts.q_splits, rows, a.heads, a.tq, a.d, c.dq,
+                             SumJob{c.parts.dq, c.dq}, SumJob{}, c.parts.q_splits, rows, a.heads, a.tq, a.d,
                              c.parts.ddelta, c.parts.delta);
           code = launch_status();
         }
@@ -110,10 +110,9 @@ int launch_bwd(const BwdCall& c) {
                          dim3(kAttnThreads), dkv_lds, c.s, a, c.q, c.k, c.v, c.dout, c.lse, c.dk, c.dv, c.parts, c.buckets);
       code = launch_status();
       if (code != RDFFT_OK || c.plan.k_splits == 1) return code;
-      for (int n = 0; n < 2; ++n)
-        hipLaunchKernelGGL((attention_sum_kernel<Io>), dim3(static_cast<unsigned>(keys)), dim3(kWave), 0, c.s,
-                           n ? c.parts.dv : c.parts.dk, c.parts.k_splits, keys, a.kv_heads, a.tk, a.d,
-                           n ? c.dv : c.dk, static_cast<const float*>(nullptr), static_cast<float*>(nullptr));
+      hipLaunchKernelGGL((attention_sum_kernel<Io>), dim3(static_cast<unsigned>(2 * keys)), dim3(kWave), 0, c.s,
+                         SumJob{c.parts.dk, c.dk}, SumJob{c.parts.dv, c.dv}, c.parts.k_splits, keys, a.kv_heads, a.tk,
+                         a.d, static_cast<const float*>(nullptr), static_cast<float*>(nullptr));
       return launch_status();
     });
   });

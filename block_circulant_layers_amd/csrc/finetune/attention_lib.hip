@@ -95,10 +95,10 @@ Plan plan_of(const attention_problem& a) {
   p.fwd_blocks = units * (group / p.pack) * ceil_div(a.queries * p.pack, kAttnRows);
   p.fwd_splits = splits_of(p.fwd_blocks, ceil_div(a.keys, kAttnKeys));
   p.dq_blocks = units * group * ceil_div(a.queries, kAttnRows);
-  p.q_splits = splits_of(p.dq_blocks, ceil_div(a.keys, kAttnKeys));
+  p.q_splits = splits_of(p.dq_blocks, ceil_div(a.keys, kAttnKeys) / 2);
   const int64_t tiles = ceil_div(a.keys, kAttnRows);
   p.dkv_blocks = units * tiles;
-  p.k_splits = splits_of(p.dkv_blocks, group * ceil_div(a.queries, kAttnKeys));
+  p.k_splits = splits_of(p.dkv_blocks, group * ceil_div(a.queries, kAttnKeys) / 2);
   const auto round4 = [](int64_t n) { return (n + 3) / 4 * 4; };
   if (p.fwd_splits > 1) p.fwd_bytes = 4 * (round4(p.fwd_splits * rows * a.head_dim) + round4(p.fwd_splits * rows * 2));
   int64_t at = 0;

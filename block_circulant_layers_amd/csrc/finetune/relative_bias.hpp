@@ -133,7 +133,8 @@ __global__ __launch_bounds__(kBiasThreads) void relative_bias_bwd_kernel(const t
   float left = 0.0f, right = 0.0f;
   for (int64_t i = i0 + wave; i < i1; i += kWaves) {
     const typename Io::T* row = dbias + h * sh + i * sq;
-    for (int64_t j = int64_t(l) * V; j < tk; j += kWave * V) {
+    for (int64_t j0 = 0; j0 < tk; j0 += kWave * V) {
+      const int64_t j = j0 + l * V;
       float s[V];
 #pragma unroll
       for (int x = 0; x < V; ++x) s[x] = 0.0f;
@@ -160,22 +161,19 @@ __global__ __launch_bounds__(kBiasThreads) void relative_bias_bwd_kernel(const t
             if (j + x < tk) s[x] += Io::widen(row[n * sb + j + x]);
       }
       const int64_t rel = j - i - (tk - tq);
-      if (rel <= -b.reach - (V - 1) || rel >= b.reach) {
-        float all = s[0];
+      const bool far = rel <= -b.reach - (V - 1) || rel >= b.reach;
+      float all = s[0];
 #pragma unroll
-        for (int x = 1; x < V; ++x) all += s[x];
-        if (rel < 0)
-          left += all;
-        else
-          right += all;
-      } else {
-        FINETUNE_WAVE_FENCE();
+      for (int x = 1; x < V; ++x) all += s[x];
+      if (far && rel < 0) left += all;
+      if (far && rel >= 0) right += all;
+      FINETUNE_WAVE_FENCE();
+      if (!far && j < tk) {
         float old[V];
 #pragma unroll
         for (int x = 0; x < V; ++x) old[x] = mine[slots.at(static_cast<int>(rel) + x)];
 #pragma unroll
         for (int x = 0; x < V; ++x) mine[slots.at(static_cast<int>(rel) + x)] = old[x] + s[x];
-        FINETUNE_WAVE_FENCE();
       }
     }
   }
