@@ -33,6 +33,8 @@ __global__ __launch_bounds__(kWave) void bias_parts_kernel(const float* part, fl
 }
 
 constexpr int64_t kUnits = 256;  // compute units
+// Buffers of a call beyond this many bytes go past the caches: they cannot be found there again.
+constexpr int64_t kCacheBytes = int64_t(320) << 20;
 
 // ---- relative position bias -----------------------------------------------
 
@@ -175,11 +177,16 @@ int relative_bias_bwd(const void* dbias, int64_t batch_stride, int64_t head_stri
     const Buckets b = buckets_of(*buckets);
     st = by_dtype(dtype, [&](auto io) {
       using Io = decltype(io);
-      hipLaunchKernelGGL((relative_bias_bwd_kernel<Io>), dim3(static_cast<unsigned>(heads * parts)),
-                         dim3(kBiasThreads), 4 * kBiasThreads / kWave * Slots(b.reach + Io::kVec).size(), s,
-                         static_cast<const typename Io::T*>(dbias), batch_stride,
-                         head_stride, query_stride, static_cast<float*>(ws), batch, queries, keys,
-                         static_cast<int>(parts), b);
+      const int lds = 4 * kBiasThreads / kWave * Slots(b.reach + Io::kVec).size();
+      const dim3 grid(static_cast<unsigned>(heads * parts));
+      const auto* from = static_cast<const typename Io::T*>(dbias);
+      auto* to = static_cast<float*>(ws);
+      if (batch * heads * queries * keys * int64_t(sizeof(typename Io::T)) > kCacheBytes)
+        hipLaunchKernelGGL((relative_bias_bwd_kernel<Io, true>), grid, dim3(kBiasThreads), lds, s, from, batch_stride,
+                           head_stride, query_stride, to, batch, queries, keys, static_cast<int>(parts), b);
+      else
+        hipLaunchKernelGGL((relative_bias_bwd_kernel<Io, false>), grid, dim3(kBiasThreads), lds, s, from, batch_stride,
+                           head_stride, query_stride, to, batch, queries, keys, static_cast<int>(parts), b);
       return launch_status();
     });
     if (st != RDFFT_OK) return st;
@@ -302,9 +309,6 @@ int attention_bwd(const attention_problem* a, const attention_tensor* q, const a
 namespace finetune {
 namespace {
 
-// Elements beyond which the buffers of a call go past the caches: they cannot be found there again.
-constexpr int64_t kDropCacheBytes = int64_t(320) << 20;
-
 template <bool RES>
 int launch_dropout(const void* x, const void* res, void* y, const DropArgs& a, int dtype, hipStream_t s) {
   return by_dtype(dtype, [&](auto io) {
@@ -318,7 +322,7 @@ int launch_dropout(const void* x, const void* res, void* y, const DropArgs& a, i
     if (!flat) {
       hipLaunchKernelGGL((dropout_rows_kernel<Io, RES>), dim3(static_cast<unsigned>(grid)), dim3(kDropThreads), 0, s,
                          px, pr, py, a);
-    } else if (n * int64_t(sizeof(T)) * (RES ? 3 : 2) > kDropCacheBytes) {
+    } else if (n * int64_t(sizeof(T)) * (RES ? 3 : 2) > kCacheBytes) {
       hipLaunchKernelGGL((dropout_kernel<Io, RES, true>), dim3(static_cast<unsigned>(grid)), dim3(kDropThreads), 0, s,
                          px, pr, py, n, a);
     } else {

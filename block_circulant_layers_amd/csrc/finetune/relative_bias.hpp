@@ -117,12 +117,12 @@ __device__ __forceinline__ void bucket_sums(const float* sums, const Slots& slot
 // row at a time, 16 bytes a lane, and sums it over the batch first.  Pieces that
 // lie beyond `reach` on one side have one bucket and stay in a register; the
 // others are added to the wave's slots.
-template <class Io>
+template <class Io, bool STREAM>
 __global__ __launch_bounds__(kBiasThreads) void relative_bias_bwd_kernel(const typename Io::T* dbias, int64_t sb,
                                                                          int64_t sh, int64_t sq, float* part,
                                                                          int64_t batch, int64_t tq, int64_t tk,
                                                                          int parts, Buckets b) {
-  constexpr int V = Io::kVec, kWaves = kBiasThreads / kWave;
+  constexpr int V = Io::kVec, kWaves = kBiasThreads / kWave, kDeep = 8;
   FINETUNE_DYNAMIC_LDS(sums);
   const Slots slots(b.reach + V);
   const int h = blockIdx.x / parts, p = blockIdx.x % parts, l = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -139,20 +139,17 @@ __global__ __launch_bounds__(kBiasThreads) void relative_bias_bwd_kernel(const t
 #pragma unroll
       for (int x = 0; x < V; ++x) s[x] = 0.0f;
       if (j + V <= tk) {
-        int64_t n = 0;
-        for (; n + 4 <= batch; n += 4) {
-          typename Io::Vec v[4];
+        for (int64_t n = 0; n < batch; n += kDeep) {  // as many loads on their way
+          typename Io::Vec v[kDeep];
 #pragma unroll
-          for (int m = 0; m < 4; ++m) v[m] = load_vec<Io>(row + (n + m) * sb + j);
+          for (int m = 0; m < kDeep; ++m) {
+            v[m] = typename Io::Vec{};
+            if (n + m < batch) v[m] = load_vec<Io, STREAM>(row + (n + m) * sb + j);
+          }
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
+          for (int m = 0; m < kDeep; ++m)
 #pragma unroll
             for (int x = 0; x < V; ++x) s[x] += Io::widen(v[m][x]);
-        }
-        for (; n < batch; ++n) {
-          const typename Io::Vec v = load_vec<Io>(row + n * sb + j);
-#pragma unroll
-          for (int x = 0; x < V; ++x) s[x] += Io::widen(v[x]);
         }
       } else {
         for (int64_t n = 0; n < batch; ++n)
