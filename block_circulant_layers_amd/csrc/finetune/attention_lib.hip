@@ -120,8 +120,8 @@ Plan plan_of(const attention_problem& a) {
   p.bwd_bytes = 4 * at;
   return p;
 }
-bool launchable(const Plan& p) {
-  return p.fwd_blocks * p.fwd_splits <= kMaxBlocks && p.dq_blocks * p.q_splits <= kMaxBlocks &&
+bool launchable(const attention_problem& a, const Plan& p) {
+  return (!a.bias || a.buckets.count * a.heads <= kMaxBlocks) && p.fwd_blocks * p.fwd_splits <= kMaxBlocks && p.dq_blocks * p.q_splits <= kMaxBlocks &&
          p.dkv_blocks * p.k_splits <= kMaxBlocks;
 }
 
@@ -202,7 +202,7 @@ int attention_workspace(const attention_problem* a, int backward, int64_t* bytes
   const int st = check_problem(a);
   if (st != RDFFT_OK) return st;
   const Plan p = plan_of(*a);
-  if (!launchable(p)) return RDFFT_ERR_SIZE;
+  if (!launchable(*a, p)) return RDFFT_ERR_SIZE;
   *bytes = backward ? p.bwd_bytes : p.fwd_bytes;
   return RDFFT_OK;
 }

@@ -68,7 +68,8 @@ __global__ __launch_bounds__(kBiasThreads) void relative_bias_fwd_kernel(const f
   const int64_t begin = part * per, end = begin + per < n ? begin + per : n;
   const int64_t off = tk - tq;
   for (int64_t e = begin + int64_t(threadIdx.x) * Io::kVec; e < end; e += kBiasThreads * Io::kVec) {
-    int64_t i = e / tk, j = e - i * tk;
+    // (a 64-bit division takes as long as the piece's store)
+    int64_t i = n >> 32 ? e / tk : static_cast<uint32_t>(e) / static_cast<uint32_t>(tk), j = e - i * tk;
     typename Io::Vec v;
 #pragma unroll
     for (int c = 0; c < Io::kVec; ++c) {

@@ -109,6 +109,7 @@ PROBLEMS = [
     (dict(bias=TABLE, buckets=Buckets(514, 500, 1)), SIZE), (dict(bias=TABLE, buckets=Buckets(8, 2, 1)), SIZE),
     (dict(bias=TABLE, buckets=Buckets(8, 1025, 1)), SIZE), (dict(bias=TABLE, buckets=Buckets(-8, 20, 1)), SIZE),
     (dict(batch=1 << 20, heads=64, kv_heads=64), SIZE),
+    (dict(batch=1, queries=1, keys=1, heads=1 << 22, bias=TABLE), SIZE),
     (dict(batch=1 << 18, heads=64, kv_heads=64, queries=1 << 24, keys=1), SIZE),
 ]
 

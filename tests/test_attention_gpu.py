@@ -175,6 +175,41 @@ def test_attention_reads_no_masked_key(dtype, queries):
     assert (lse0[-1] == -torch.inf).all() and not o0[-1].any() and not g0[0][-1].any() and not g0[1][-1].any()
 
 
+def test_attention_spans_are_clamped():
+    """Ends past the keys, negative begins, ends before begins."""
+    x, kw, _, _ = au.case((15,), 4, 70, 90, 2, 1, 32, "bf16")
+    q, k, v, do = (x[n][0] for n in ("q", "k", "v", "dout"))
+
+    def both(begin, end):
+        spans = dict(key_begin=torch.tensor(begin, device=DEV, dtype=torch.int32),
+                     key_end=torch.tensor(end, device=DEV, dtype=torch.int32))
+        o, lse = bcl.attention_fwd(q, k, v, **kw, **spans)
+        return [o, lse, *bcl.attention_bwd(q, k, v, o, lse, do, **kw, **spans)[:3]]
+
+    big = (1 << 31) - 1
+    for a, b in zip(both([-5, 10, 60, big], [big, 50, 20, big]), both([0, 10, 60, 90], [90, 50, 60, 90])):
+        assert torch.equal(a, b)
+
+
+def test_attention_bias_of_minus_infinity():
+    """A bucket that is ruled out takes no part; a query left with such buckets alone sees no key."""
+    x, kw, see, bias = au.case((16,), 1, 60, 60, 2, 2, 32, "f32", table=7, two_sided=False, causal=True)
+    q, k, v, do = (x[n][0] for n in ("q", "k", "v", "dout"))
+    kw["bias"][0] = -torch.inf  # a query's own position: the first query has no other
+    where = ao.bucket_matrix(60, 60, 7, kw["max_distance"], False)
+    see = see & (where != 0)
+    o, lse = bcl.attention_fwd(q, k, v, **kw)
+    want, want_lse, p = ao.attention(*(x[n][1] for n in "qkv"), kw["scale"], see, bias)
+    bo, bl = au.forward_bounds(*(x[n][1] for n in "qkv"), kw["scale"], want, want_lse, p, "f32", bias)
+    within(f64(o), want, bo)
+    within(f64(lse), want_lse, bl)
+    grads = bcl.attention_bwd(q, k, v, o, lse, do, **kw)
+    for got, exact in zip(grads[:3], ao.attention_bwd(*(x[n][1] for n in "qkv"), p, x["dout"][1], kw["scale"])):
+        # fp32 throughout, sums of at most 60 terms of either sign
+        assert np.linalg.norm(f64(got) - exact) <= 1e-5 * np.linalg.norm(exact)
+    assert not grads[3][0].any() and grads[3].isfinite().all() and not o[0, 0].any()
+
+
 @pytest.mark.parametrize("bias", [False, True])
 def test_attention_of_nothing(bias):
     kw = dict(bias=torch.ones(8, 2, device=DEV)) if bias else {}
