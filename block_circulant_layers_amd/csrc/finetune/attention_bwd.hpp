@@ -11,7 +11,7 @@
 //
 // Bound by LDS latency at two waves a SIMD (dq) or one (dk and dv of more than 64
 // elements, whose sums, keys and values take 192 registers): 2 x 4096 causal
-// tokens, 32 heads over 8 of 128, bf16 660 and 1030 us, 410 TFLOP/s of the five
+// tokens, 32 heads over 8 of 128, bf16 670 and 950 us, 430 TFLOP/s of the five
 // products together; 2 x 4096, 32 heads of 64 1340 us, 510 TFLOP/s.
 #pragma once
 
@@ -27,10 +27,15 @@ template <class Io, int DP>
 constexpr bool kBwdTight = sizeof(typename Io::T) == 4 && DP > 64;
 template <class Io, int DP>
 constexpr int kBwdQueries = kBwdTight<Io, DP> ? 32 : 64;
+// floats in LDS of such a step: the tiles of q and dout, and for each query kLift - lse in log2 units, -delta, peak
+template <class Io, int DP>
+constexpr int kTileSet = 2 * Tile<Io, DP>::bytes(kBwdQueries<Io, DP>) / 4 + 3 * kBwdQueries<Io, DP>;
 
+// Waves a SIMD that the registers are cut for.  On the long case above dq took 830 us at one wave and 530 at two (before
+// ds had two parts); dk and dv 1040 us at one, where two keep registers in memory or the values in LDS (1104 us).
 template <class Io, int DP, bool BIAS>
 constexpr int kDqWaves = (sizeof(typename Io::T) == 4 && DP > 32) || (BIAS && DP > 96) ? 1 : 2;
-// operands fetched ahead by the kernel of dq, of N
+// operands fetched ahead by the kernel of dq, of N: four at 128 elements keep registers in memory (590 us against 530)
 template <class Io, int DP, int N>
 constexpr int kDqGroup = DP > 96 ? 0 : kAheadOf<Io, N>;
 template <class Io, int DP, bool BIAS>
@@ -244,12 +249,10 @@ __global__ __launch_bounds__(kAttnThreads, (kDkvWaves<Io, DP, BIAS>)) void atten
   constexpr bool kScaled = std::is_same_v<Io, F16>, kNarrow = sizeof(T) == 4;
   constexpr int DC = DP / 16, DB = DP / 32, QN = kBwdQueries<Io, DP>, QB = QN / 32;
   FINETUNE_DYNAMIC_LDS(attention_lds);
-  T* sq = reinterpret_cast<T*>(attention_lds);
-  T* sd = sq + L::bytes(QN) / sizeof(T);
-  float* sbase = reinterpret_cast<float*>(sd + L::bytes(QN) / sizeof(T));  // kLift - lse in log2 units
-  float* sdelta = sbase + QN;
-  float* speak = sdelta + QN;
-  float* line = speak + QN;
+  // two sets of tiles and of their queries' numbers in turn, so that one is written while slower waves read the other:
+  // one barrier a tile (at one wave a SIMD 1010 -> 950 us on the long case; the forward, at two, 420 -> 435)
+  constexpr int kTile = L::bytes(QN) / sizeof(T), kSet = kTileSet<Io, DP>;
+  float* line = attention_lds + 2 * kSet;
   const Slots slots(BIAS ? buckets.reach + kEdge : 0);
   float* sums = line + (BIAS ? bias_line(buckets) : 0);  // of ds by relative position, a wave's after another's
   float* mine = sums + threadIdx.x / kWave * slots.size();
@@ -298,6 +301,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDkvWaves<Io, DP, BIAS>)) void atten
   for (int n = 0; n < DB; ++n) ak[n] = zero_acc(), av[n] = zero_acc();
   float power = 1.0f;  // fp16: what ds is formed times
   bool first = true;
+  int turn = 0;
 
   using Rows = Stage<Io, DP, QN, kAttnThreads>;
   Rows nx, nd;
@@ -335,8 +339,11 @@ __global__ __launch_bounds__(kAttnThreads, (kDkvWaves<Io, DP, BIAS>)) void atten
     constexpr bool kAhead = !kBwdTight<Io, DP>;
     if (kAhead && qa < qb) fetch(qa), fetch_dout(qa);
     for (int t = qa; t < qb; ++t) {
+      float* set = attention_lds + turn * kSet;
+      T *sq = reinterpret_cast<T*>(set), *sd = sq + kTile;
+      float *sbase = reinterpret_cast<float*>(sd + kTile), *sdelta = sbase + QN, *speak = sdelta + QN;
+      turn = 1 - turn;
       if (!kAhead) fetch(t);
-      __syncthreads();
       const auto mend = [&](Rows& x) {  // rows of queries without a key may hold anything
         if (!holes) return;
 #pragma unroll
@@ -373,7 +380,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDkvWaves<Io, DP, BIAS>)) void atten
       }
       const float unlift = kScaled ? 0.00390625f : 1.0f;
       const float fs = power * unlift;
-#pragma unroll 1
+#pragma unroll DP > 64 ? QB : 1
       for (int n = 0; n < QB; ++n) {
         const int r0 = i0 + 32 * n;
         if (a.causal && r0 + 31 + off < w0) continue;  // no query of the block sees a key of the wave

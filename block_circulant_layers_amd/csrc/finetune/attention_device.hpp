@@ -204,7 +204,8 @@ __device__ __forceinline__ void fetched_ahead(L load, U use) {
     for (int i = 0; i < G; ++i) use(s * G + i, f[s % 2][i]);
   }
 }
-// how many operands ahead, of N: four of the 16-bit types
+// how many operands ahead, of N: four of the 16-bit types (dk and dv of the long case in attention_bwd.hpp 1240 us
+// without, 1040 with; the forward the same either way)
 template <class Io, int N>
 constexpr int kAheadOf = sizeof(typename Io::T) == 4 ? 0 : N % 4 == 0 ? 4 : N % 2 == 0 ? 2 : 0;
 

@@ -89,7 +89,7 @@ int launch_bwd(const BwdCall& c) {
       constexpr bool kBias = decltype(bias)::value;
       const int line = kBias ? 4 * bias_line(c.buckets) : 0;
       const int dq_lds = 2 * Tile<Io, DP>::bytes(kAttnKeys) + line;
-      const int dkv_lds = 2 * Tile<Io, DP>::bytes(kBwdQueries<Io, DP>) + 3 * 4 * kBwdQueries<Io, DP> +
+      const int dkv_lds = 2 * 4 * kTileSet<Io, DP> +
                           (kBias ? line + 4 * 4 * (kBlockFloats + Slots(c.buckets.reach + kEdge).size()) : 0);
       int code = RDFFT_OK;
       if (c.plan.dq_blocks > 0) {

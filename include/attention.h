@@ -100,7 +100,8 @@ int attention_workspace(const attention_problem* a, int backward, int64_t* bytes
  *   o   like q, written; must not overlap q, k, v
  *   lse [batch, heads, queries]  float, written
  * Products take the storage type with fp32 sums; p is rounded to the storage
- * type for its product with v.
+ * type for its product with v.  Infinities and NaN of keys and values that some
+ * query sees may also reach queries nearby that do not see them (0 times them).
  */
 int attention_fwd(const attention_problem* a, const attention_tensor* q, const attention_tensor* k,
                   const attention_tensor* v, const attention_tensor* o, float* lse, void* ws, int64_t ws_bytes,
