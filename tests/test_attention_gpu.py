@@ -78,6 +78,11 @@ def test_attention_bias_buckets(table, distance, two_sided):
     check((1, 350, 420, 2, 2, 32), "f32", "bias", table=table, distance=distance, two_sided=two_sided)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_attention_bias_at_the_largest_lds(dtype):
+    check((1, 90, 140, 2, 1, 128), dtype, "bias", table=512, distance=1024)
+
+
 def test_attention_bias_of_shared_heads():
     check((2, 70, 90, 4, 2, 32), "bf16", "bias")
     check((1, 1, 600, 8, 2, 64), "f32", "bias_one_sided")
