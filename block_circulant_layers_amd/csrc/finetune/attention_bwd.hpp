@@ -207,7 +207,8 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<Io, DP, BIAS>)) void attent
   }
   along = halves_sum(along);
   if (i >= a.tq) return;
-  const float out_scale = live ? a.scale / power : 0.0f;
+  const float out_scale = a.scale / power;
+  const auto value = [&](float x) { return live ? x * out_scale : 0.0f; };
   // The other kernel gets delta as the sum of p dp: o is rounded, and its error would stand in every sum over queries.
   delta = live ? along * unlift : 0.0f;
   const int64_t all = int64_t(a.batch) * a.heads * a.tq, at = row0 + i;
@@ -224,8 +225,8 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<Io, DP, BIAS>)) void attent
     for (int n = 0; n < DB; ++n)
 #pragma unroll
       for (int r = 0; r < 16; r += 4)
-        store_four<F32>(out, 32 * n + 2 * r + 4 * g, a.d, acc[n][r] * out_scale, acc[n][r + 1] * out_scale,
-                        acc[n][r + 2] * out_scale, acc[n][r + 3] * out_scale);
+        store_four<F32>(out, 32 * n + 2 * r + 4 * g, a.d, value(acc[n][r]), value(acc[n][r + 1]),
+                        value(acc[n][r + 2]), value(acc[n][r + 3]));
     return;
   }
   T* out = dq.at<T>(b, i, h);
@@ -233,8 +234,8 @@ __global__ __launch_bounds__(kAttnThreads, (kDqWaves<Io, DP, BIAS>)) void attent
   for (int n = 0; n < DB; ++n)
 #pragma unroll
     for (int r = 0; r < 16; r += 4)
-      store_four<Io>(out, 32 * n + 2 * r + 4 * g, a.d, acc[n][r] * out_scale, acc[n][r + 1] * out_scale,
-                     acc[n][r + 2] * out_scale, acc[n][r + 3] * out_scale);
+      store_four<Io>(out, 32 * n + 2 * r + 4 * g, a.d, value(acc[n][r]), value(acc[n][r + 1]),
+                     value(acc[n][r + 2]), value(acc[n][r + 3]));
 }
 
 // Scores are computed queries x keys here, so that a lane has all its scores of

@@ -191,14 +191,15 @@ __global__ __launch_bounds__(kAttnThreads, (kFwdWaves<Io, DP, BIAS>)) void atten
     }
     return;
   }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const float inv = 1.0f / total;
+  const auto value = [&](float x) { return total == 0.0f ? 0.0f : x * inv; };  // (0 also beside values of infinity)
   T* out = o.at<T>(b, i, h);
 #pragma unroll
   for (int n = 0; n < DB; ++n)
 #pragma unroll
     for (int r = 0; r < 16; r += 4)
-      store_four<Io>(out, 32 * n + 2 * r + 4 * g, a.d, acc[n][r] * inv, acc[n][r + 1] * inv, acc[n][r + 2] * inv,
-                     acc[n][r + 3] * inv);
+      store_four<Io>(out, 32 * n + 2 * r + 4 * g, a.d, value(acc[n][r]), value(acc[n][r + 1]), value(acc[n][r + 2]),
+                     value(acc[n][r + 3]));
   if (g == 0) lse[at] = total == 0.0f ? -INFINITY : (top - kLift<Io> + log2f(total)) * kLn2;
 }
 
@@ -239,9 +240,9 @@ __global__ __launch_bounds__(kWave* LANES) void attention_join_kernel(Problem a,
   const int i = static_cast<int>(at % a.tq);
   const int64_t bh = at / a.tq;
   T* out = o.at<T>(bh / a.heads, i, bh % a.heads);
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  if (l < a.d) out[l] = Io::narrow(x * inv);
-  if (l + kWave < a.d) out[l + kWave] = Io::narrow(y * inv);
+  const float inv = 1.0f / total;
+  if (l < a.d) out[l] = Io::narrow(total == 0.0f ? 0.0f : x * inv);
+  if (l + kWave < a.d) out[l + kWave] = Io::narrow(total == 0.0f ? 0.0f : y * inv);
   if (threadIdx.x == 0) lse[at] = total == 0.0f ? -INFINITY : (top - kLift<Io> + log2f(total)) * kLn2;
 }
 

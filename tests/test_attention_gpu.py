@@ -215,6 +215,19 @@ def test_attention_bias_of_minus_infinity():
     assert not grads[3][0].any() and grads[3].isfinite().all() and not o[0, 0].any()
 
 
+@pytest.mark.parametrize("tk", [40, 900])
+def test_queries_without_keys_stay_zero_beside_infinities(tk):
+    """Causal, more queries than keys: the first ones see none, whatever the keys hold that others see."""
+    x, kw, _, _ = au.case((17, tk), 1, tk + 20, tk, 2, 2, 32, "bf16", causal=True)
+    q, k, v, do = (x[n][0] for n in ("q", "k", "v", "dout"))
+    v[0, 0] = torch.inf
+    k[0, 1] = torch.nan
+    o, lse = bcl.attention_fwd(q, k, v, **kw)
+    assert not o[:, :20].any() and (lse[:, :, :20] == -torch.inf).all()
+    dq = bcl.attention_bwd(q, k, v, o, lse, do, **kw)[0]
+    assert not dq[:, :20].any()
+
+
 @pytest.mark.parametrize("bias", [False, True])
 def test_attention_of_nothing(bias):
     kw = dict(bias=torch.ones(8, 2, device=DEV)) if bias else {}
